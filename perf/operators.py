@@ -32,43 +32,43 @@ def listed():
     gqa = {"q_heads": 32, "kv_heads": 8, "dim": 128, "block": 16, "dtype": "bf16"}
     return [
         # the step of a decode batch: 256 new tokens, text positions
-        {"name": "rope, decode step", "op": "rope", **gqa, "tokens": 256, "rotary": 128,
+        {"name": "rope decode step", "op": "rope", **gqa, "tokens": 256, "rotary": 128,
          "axes": 1, "pairs": False, "fp8": True},
         # prompts with images, 16K tokens: time, height and width positions
-        {"name": "rope, image prompts", "op": "rope", **gqa, "tokens": 16384, "rotary": 128,
+        {"name": "rope image prompts", "op": "rope", **gqa, "tokens": 16384, "rotary": 128,
          "axes": 3, "pairs": False, "fp8": True},
         # one user, small heads: the latency of a call
-        {"name": "decode, one sequence", "op": "decode", "q_heads": 4, "kv_heads": 4, "dim": 64,
+        {"name": "decode one sequence", "op": "decode", "q_heads": 4, "kv_heads": 4, "dim": 64,
          "block": 16, "dtype": "f16", "seqs": 1, "low": 777, "high": 777, "mix": 1},
         # a serving batch of mixed lengths, 16 to 4096 tokens
-        {"name": "decode, mixed batch", "op": "decode", **gqa, "seqs": 256, "low": 16,
+        {"name": "decode mixed batch", "op": "decode", **gqa, "seqs": 256, "low": 16,
          "high": 4096, "mix": 2},
         # a few long documents, 16K to 32K tokens, wide groups
-        {"name": "decode, long contexts", "op": "decode", "q_heads": 64, "kv_heads": 8,
+        {"name": "decode long contexts", "op": "decode", "q_heads": 64, "kv_heads": 8,
          "dim": 128, "block": 32, "dtype": "bf16", "seqs": 8, "low": 16384, "high": 32768,
          "mix": 3},
         # short last chunks after long cached prefixes: few rows, many keys
-        {"name": "prompt, chunks on prefixes", "op": "prompt", "q_heads": 64, "kv_heads": 8,
+        {"name": "prompt chunks on prefixes", "op": "prompt", "q_heads": 64, "kv_heads": 8,
          "dim": 128, "dtype": "bf16", "seqs": 3, "low": 5, "high": 40, "before_low": 4000,
          "before_high": 16000, "mix": 4},
         # a batch of fresh prompts of mixed lengths, no grouped heads
-        {"name": "prompt, ragged batch", "op": "prompt", "q_heads": 40, "kv_heads": 40,
+        {"name": "prompt ragged batch", "op": "prompt", "q_heads": 40, "kv_heads": 40,
          "dim": 128, "dtype": "f16", "seqs": 16, "low": 64, "high": 2048, "before_low": 0,
          "before_high": 0, "mix": 5},
         # one long prompt
-        {"name": "prompt, one of 8192", "op": "prompt", "q_heads": 32, "kv_heads": 8, "dim": 128,
+        {"name": "prompt one of 8192", "op": "prompt", "q_heads": 32, "kv_heads": 8, "dim": 128,
          "dtype": "bf16", "seqs": 1, "low": 8192, "high": 8192, "before_low": 0,
          "before_high": 0, "mix": 6},
         # a prefix hit of one request
-        {"name": "gather, one prefix", "op": "gather", **gqa, "seqs": 1, "low": 300, "high": 300,
+        {"name": "gather one prefix", "op": "gather", **gqa, "seqs": 1, "low": 300, "high": 300,
          "mix": 7},
         # the cached contexts of a batch of chunks
-        {"name": "gather, batch of contexts", "op": "gather", **gqa, "seqs": 16, "low": 512,
+        {"name": "gather batch of contexts", "op": "gather", **gqa, "seqs": 16, "low": 512,
          "high": 8192, "mix": 8},
         # the copies of one step of forked sequences
-        {"name": "copy, one step", "op": "copy", **gqa, "pairs": 37},
+        {"name": "copy one step", "op": "copy", **gqa, "pairs": 37},
         # every branch of many forks writes for the first time
-        {"name": "copy, first writes", "op": "copy", **gqa, "pairs": 2048},
+        {"name": "copy first writes", "op": "copy", **gqa, "pairs": 2048},
     ]
 
 
