@@ -77,6 +77,7 @@ typedef enum {
 #define PA_DEVERR_RANGE 0x20u      /* prefill over a bf16 cache: an output row came out not
                                       finite -- a V value beyond fp16's range (|v| >= 65520)
                                       or a non-finite q, K or V element */
+#define PA_DEVERR_POSITION 0x40u   /* rotary position outside [0, max_position) */
 
 /* Human-readable name of a pa_status value (static string). */
 const char *pa_status_string(int status);
@@ -309,6 +310,120 @@ int pa_paged_prefill_attention(float *out, const void *q, const void *k_cache,
                                int num_q_heads, int head_dim, int block_size,
                                int max_blocks_per_seq, int max_query_len, int num_blocks,
                                pa_dtype dtype, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions, an 8-bit cache and whole prompts.  No counterpart on the
+ * pages: what an engine needs around the calls above.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * Rotary positions on the queries and keys of num_tokens new tokens, and the
+ * write of their K/V into the 16-bit pool, in one pass.  Frequency pair j
+ * (0 <= j < rotary_dim / 2) of every q and k head is turned by the angle of
+ * the position that its axis gives:
+ *   a' = a cos - b sin,  b' = b cos + a sin,   in fp32, rounded once,
+ * (a, b) = columns (j, j + rotary_dim/2), or (2j, 2j + 1) if `interleaved`.
+ * Columns from rotary_dim on, and V, pass unchanged.
+ *
+ *   q_out         dtype [num_tokens, num_q_heads, head_dim] (device, written);
+ *                 may be q itself with the same stride, else must not overlap it
+ *   q             dtype, same shape; NULL: no queries, q_out is not used
+ *   key, value    dtype [num_tokens, num_kv_heads, head_dim] (device)
+ *   *_stride      elements from one token's row to the next (the heads of a
+ *                 token are dense): at least heads * head_dim, a multiple of
+ *                 8; so q, key and value may be columns of one projection
+ *   slot_mapping  int64 [num_tokens], as for pa_reshape_and_cache: slot < 0
+ *                 skips the cache write (q is still turned), a slot outside
+ *                 the pool is skipped and sets PA_DEVERR_SLOT
+ *   positions     int64 [num_axes, num_tokens] (device).  A token with a
+ *                 position outside [0, max_position) on any axis is skipped
+ *                 altogether (neither q_out nor the cache is written) and
+ *                 sets PA_DEVERR_POSITION
+ *   cos_sin       fp32 [max_position, rotary_dim] (device): the rotary_dim/2
+ *                 cosines of a position, then its sines
+ *   sections      host int [num_axes]: how many consecutive frequency pairs
+ *                 take their position from each axis; they sum to
+ *                 rotary_dim / 2.  One axis for text; (time, height, width)
+ *                 for images and video.  num_axes is 1 to 4
+ *   rotary_dim    a multiple of 16, at most head_dim; 0 turns nothing (then
+ *                 positions, cos_sin and sections are not used)
+ * Two tokens with the same slot in one call: which one lands is undefined.
+ * num_tokens == 0 launches nothing.  num_q_heads may be any number (groups
+ * play no part here).
+ */
+int pa_rope_and_cache(void *q_out, const void *q, const void *key, const void *value,
+                      void *k_cache, void *v_cache, const int64_t *slot_mapping,
+                      const int64_t *positions, const float *cos_sin, const int *sections,
+                      int num_axes, int rotary_dim, int max_position, int interleaved,
+                      int64_t q_out_stride, int64_t q_stride, int64_t key_stride,
+                      int64_t value_stride, int num_tokens, int num_q_heads, int num_kv_heads,
+                      int head_dim, int block_size, int num_blocks, pa_dtype dtype,
+                      pa_stream_t stream);
+
+/*
+ * The 8-bit pool of the _fp8 calls:
+ *   k_cache, v_cache  e4m3 codes [num_blocks, num_kv_heads, block_size, head_dim]
+ *   kv_scale          fp32 [num_blocks, num_kv_heads, 2, block_size]: the scale
+ *                     of each token's K row (index 0) and V row (index 1)
+ * A cached element is code * scale.  A row is written with
+ *   scale = max(amax, 2^-100) / 448,  code = e4m3(x * (448 / max(amax, 2^-100)))
+ * (round to nearest even), amax the row's largest magnitude, so an element is
+ * off by at most 2^-4 of itself or 2^-10 * scale, whichever is more.  A row
+ * with an infinite element reads back as NaN, a NaN element as NaN.
+ *
+ * pa_rope_and_cache_fp8 is pa_rope_and_cache into this pool: the codes are made
+ * from the fp32 turned keys (not from their 16-bit rounding), and the row's
+ * scales are written with them.
+ */
+int pa_rope_and_cache_fp8(void *q_out, const void *q, const void *key, const void *value,
+                          void *k_cache, void *v_cache, float *kv_scale,
+                          const int64_t *slot_mapping, const int64_t *positions,
+                          const float *cos_sin, const int *sections, int num_axes, int rotary_dim,
+                          int max_position, int interleaved, int64_t q_out_stride,
+                          int64_t q_stride, int64_t key_stride, int64_t value_stride,
+                          int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                          int block_size, int num_blocks, pa_dtype dtype, pa_stream_t stream);
+
+/*
+ * pa_paged_decode_attention over the 8-bit pool: the same arguments, masks,
+ * workspace (pa_paged_decode_workspace_bytes) and errors, plus kv_scale; q of
+ * dtype, out fp32.  Accumulated in fp32 with the weights carried to 2^-22, so
+ * the output is that of the cached values (code * scale) to ~1e-6.
+ */
+int pa_paged_decode_attention_fp8(float *out, const void *q, const void *k_cache,
+                                  const void *v_cache, const float *kv_scale,
+                                  const int32_t *block_tables, const int32_t *context_lens,
+                                  float scale, int num_kv_heads, int num_seqs, int num_q_heads,
+                                  int head_dim, int block_size, int max_blocks_per_seq,
+                                  int max_context_len, int num_blocks, pa_dtype dtype,
+                                  void *workspace, size_t workspace_bytes, pa_stream_t stream);
+
+/*
+ * pa_copy_blocks on the 8-bit pool: a block's codes of K and V and its scales.
+ * Same block_mapping, precondition and errors (any number of pairs).
+ */
+int pa_copy_blocks_fp8(void *k_cache, void *v_cache, float *kv_scale, const int64_t *block_mapping,
+                       int num_pairs, int num_kv_heads, int head_dim, int block_size,
+                       int num_blocks, pa_stream_t stream);
+
+/*
+ * Cached rows out of the 8-bit pool, packed and in 16 bits: rows key_start[s]
+ * .. key_start[s+1]-1 of key and value become positions 0, 1, ... of sequence
+ * s, each element code * scale rounded to dtype.  With it a chunk of new
+ * tokens can attend over a cached prefix through pa_prompt_attention.
+ *
+ *   key, value    dtype [num_tokens, num_kv_heads, head_dim] (device, written)
+ *   block_tables  int32 [num_seqs, max_blocks_per_seq] (device)
+ *   key_start     int32 [num_seqs + 1] (device), non-decreasing
+ * Rows from key_start[num_seqs] on are left as they were.  A position beyond
+ * the table sets PA_DEVERR_CONTEXT_LEN, a block id outside the pool
+ * PA_DEVERR_BLOCK_ID; their rows are left as they were.
+ */
+int pa_gather_cache_fp8(void *key, void *value, const void *k_cache, const void *v_cache,
+                        const float *kv_scale, const int32_t *block_tables,
+                        const int32_t *key_start, int num_seqs, int num_tokens, int num_kv_heads,
+                        int head_dim, int block_size, int max_blocks_per_seq, int num_blocks,
+                        pa_dtype dtype, pa_stream_t stream);
 
 /*
  * Read the sticky device error word of the current device into *flags

@@ -9,8 +9,10 @@ missing or a call fails, an exception is raised.
 Names follow the C ABI: ``pa_reshape_and_cache``, ``pa_paged_decode_attention``
 (with ``pa_paged_decode_workspace_bytes``, and ``pa_paged_decode_attention_no_alloc``),
 the fused ``pa_decode_step``, ``pa_paged_prefill_attention`` (chunked prefill),
-``pa_copy_blocks``, ``pa_device_error``, ``pa_decode_tuning``, ``pa_set_wait_limit``,
-and the host block manager ``BlockManager`` over the ``pa_bm_*`` calls (prefix
+``pa_copy_blocks``, ``pa_device_error``, ``pa_decode_tuning``, ``pa_set_wait_limit``;
+rotary positions with the cache write, ``pa_rope_and_cache``; the 8-bit pool's
+``pa_rope_and_cache_fp8``, ``pa_paged_decode_attention_fp8``, ``pa_gather_cache_fp8``
+and ``pa_copy_blocks_fp8``; and the host block manager ``BlockManager`` over the ``pa_bm_*`` calls (prefix
 caching included).
 """
 from __future__ import annotations
@@ -27,7 +29,7 @@ PA_F16, PA_BF16 = 0, 1
 STATUS = {0: "PA_OK", -1: "PA_ERR_ARG", -2: "PA_ERR_UNSUPPORTED", -3: "PA_ERR_NO_BLOCKS",
           -4: "PA_ERR_SEQ", -5: "PA_ERR_CUDA", -6: "PA_ERR_DEVICE_BOUNDS", -7: "PA_ERR_WORKSPACE"}
 DEVERR = {"block_id": 0x1, "context_len": 0x2, "slot": 0x4, "copy_pair": 0x8, "timeout": 0x10,
-          "range": 0x20}
+          "range": 0x20, "position": 0x40}
 
 
 class PAError(RuntimeError):
@@ -84,6 +86,11 @@ def _declare(L):
         "pa_set_wait_limit": (i32, [c.c_longlong]),
         "pa_paged_prefill_attention": (i32, [vp, vp, vp, vp, vp, vp, vp, f32, i32, i32, i32, i32,
                                              i32, i32, i32, i32, i32, i32, vp]),
+        "pa_rope_and_cache": (i32, [vp] * 10 + [i32] * 4 + [i64] * 4 + [i32] * 7 + [vp]),
+        "pa_rope_and_cache_fp8": (i32, [vp] * 11 + [i32] * 4 + [i64] * 4 + [i32] * 7 + [vp]),
+        "pa_paged_decode_attention_fp8": (i32, [vp] * 7 + [f32] + [i32] * 9 + [vp, sz, vp]),
+        "pa_copy_blocks_fp8": (i32, [vp] * 4 + [i32] * 5 + [vp]),
+        "pa_gather_cache_fp8": (i32, [vp] * 7 + [i32] * 8 + [vp]),
         "pa_copy_blocks": (i32, [vp, vp, vp, i32, i32, i32, i32, i32, i32, vp]),
         "pa_device_error": (i32, [c.POINTER(c.c_uint), i32]),
         "pa_bm_create": (vp, [i32, i32, P32]),
@@ -331,6 +338,190 @@ def pa_device_error(clear: bool = True) -> int:
     if st not in (0, -6):
         _check(st, "pa_device_error")
     return int(v.value)
+
+
+# ------------------------------------------------- rotary positions, 8-bit pool, prompts
+
+def _here(**tensors):
+    """Every tensor given lies on the current CUDA device, where the call launches."""
+    torch = _torch()
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is {dev}")
+
+
+def _flat(t, name, dtype, shape):
+    """Pointer of a dense tensor of that dtype and shape (None: any size)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} must be {['any' if n is None else n for n in shape]}, "
+                         f"got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t, name, dtype, shape):
+    """(pointer, row stride in elements) of [tokens, heads, head_dim] whose tokens may lie
+    apart (columns of a fused projection) and whose heads are dense."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    n, h, d = shape
+    s0, s1, s2 = t.stride()
+    if n > 0 and (s2 != 1 or (h > 1 and s1 != d)):
+        raise ValueError(f"{name}: the heads of a token must be dense")
+    if n <= 1:
+        s0 = h * d
+    elif s0 < h * d or s0 % 8:
+        raise ValueError(f"{name}: token stride {s0} must be a multiple of 8, at least {h * d}")
+    return t.data_ptr(), s0
+
+
+def _pool_fp8(k_cache, v_cache, kv_scale):
+    torch = _torch()
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [num_blocks, num_kv_heads, block_size, head_dim]")
+    NB, Hkv, B, D = k_cache.shape
+    return (_flat(k_cache, "k_cache", torch.float8_e4m3fn, (NB, Hkv, B, D)),
+            _flat(v_cache, "v_cache", torch.float8_e4m3fn, (NB, Hkv, B, D)),
+            _flat(kv_scale, "kv_scale", torch.float32, (NB, Hkv, 2, B)))
+
+
+def _rope(name, q_out, q, key, value, pool, caches, slot_mapping, positions, cos_sin, sections,
+          interleaved, stream):
+    torch = _torch()
+    NB, Hkv, B, D = caches.shape
+    T = key.shape[0]
+    dt = key.dtype
+    code = _dtype_code(key)
+    k, ks = _rows(key, "key", dt, (T, Hkv, D))
+    v, vs = _rows(value, "value", dt, (T, Hkv, D))
+    slots = _flat(slot_mapping, "slot_mapping", torch.int64, (T,))
+    Hq = qs = qos = 0
+    qp = qo = None
+    if q is not None:
+        Hq = q.shape[1] if q.dim() == 3 else 0
+        qp, qs = _rows(q, "q", dt, (T, Hq, D))
+        qo, qos = _rows(q_out, "q_out", dt, (T, Hq, D))
+    rot = axes = most = 0
+    pos = table = sect = None
+    if cos_sin is not None:
+        most, rot = cos_sin.shape if cos_sin.dim() == 2 else (0, 0)
+        table = _flat(cos_sin, "cos_sin", torch.float32, (most, rot))
+        axes = positions.shape[0] if positions.dim() == 2 else 1
+        pos = _flat(positions, "positions", torch.int64,
+                    (axes, T) if positions.dim() == 2 else (T,))
+        sections = (rot // 2,) if sections is None else tuple(int(n) for n in sections)
+        if len(sections) != axes:
+            raise ValueError(f"sections must name every axis: {axes} of them, got {len(sections)}")
+        sect = (ctypes.c_int * axes)(*sections)
+    st = getattr(lib(), name)(qo, qp, k, v, *pool, slots, pos, table, sect, axes, rot, most,
+                              1 if interleaved else 0, qos, qs, ks, vs, T, Hq, Hkv, D, B, NB, code,
+                              _stream(stream))
+    _check(st, name)
+
+
+def pa_rope_and_cache(q_out, q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin,
+                      sections=None, interleaved=False, stream=None):
+    """Rotary positions on q (into q_out, which may be q) and on key, and the write of key and
+    value into their slots of the 16-bit pool, in one pass.
+
+    q, q_out [T, Hq, D], key, value [T, Hkv, D]: 16 bits, heads dense, tokens any multiple of 8
+    elements apart (so they may be columns of one projection); q None: keys only.
+    positions int64 [T] or [axes, T]; cos_sin fp32 [max_position, rotary_dim], cosines then sines;
+    sections: frequency pairs of each axis, e.g. (16, 24, 24) for time, height and width (default:
+    one axis); interleaved: pairs are columns (2j, 2j+1) instead of (j, j + rotary_dim/2).
+    cos_sin None stores without turning."""
+    _here(q_out=q_out, q=q, key=key, value=value, k_cache=k_cache, v_cache=v_cache,
+          slot_mapping=slot_mapping, positions=positions, cos_sin=cos_sin)
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [num_blocks, num_kv_heads, block_size, head_dim]")
+    pool = tuple(_flat(c, n, key.dtype, tuple(k_cache.shape))
+                 for c, n in ((k_cache, "k_cache"), (v_cache, "v_cache")))
+    _rope("pa_rope_and_cache", q_out, q, key, value, pool, k_cache, slot_mapping, positions,
+          cos_sin, sections, interleaved, stream)
+
+
+def pa_rope_and_cache_fp8(q_out, q, key, value, k_cache, v_cache, kv_scale, slot_mapping,
+                          positions, cos_sin, sections=None, interleaved=False, stream=None):
+    """pa_rope_and_cache into the 8-bit pool: k_cache, v_cache float8_e4m3fn [num_blocks, Hkv, B, D]
+    and kv_scale fp32 [num_blocks, Hkv, 2, B], one scale per token's K row and V row."""
+    _here(q_out=q_out, q=q, key=key, value=value, k_cache=k_cache, v_cache=v_cache,
+          kv_scale=kv_scale, slot_mapping=slot_mapping, positions=positions, cos_sin=cos_sin)
+    _rope("pa_rope_and_cache_fp8", q_out, q, key, value, _pool_fp8(k_cache, v_cache, kv_scale),
+          k_cache, slot_mapping, positions, cos_sin, sections, interleaved, stream)
+
+
+def pa_paged_decode_attention_fp8(out, q, k_cache, v_cache, kv_scale, block_tables, context_lens,
+                                  scale, num_kv_heads, max_context_len=None, workspace=None,
+                                  stream=None):
+    """pa_paged_decode_attention over the 8-bit pool: out[s, h] = softmax(scale * q[s, h] K_s^T) V_s
+    with K and V the cached codes times their scales; q 16 bits, out fp32."""
+    torch = _torch()
+    _here(out=out, q=q, k_cache=k_cache, v_cache=v_cache, kv_scale=kv_scale,
+          block_tables=block_tables, context_lens=context_lens, workspace=workspace)
+    pool = _pool_fp8(k_cache, v_cache, kv_scale)
+    NB, Hkv, B, D = k_cache.shape
+    if q.dim() != 3 or Hkv != num_kv_heads:
+        raise ValueError("q / cache shapes disagree")
+    S, Hq = q.shape[:2]
+    code = _dtype_code(q)
+    args = (_flat(out, "out", torch.float32, (S, Hq, D)), _flat(q, "q", q.dtype, (S, Hq, D)),
+            *pool, _flat(block_tables, "block_tables", torch.int32, (S, None)),
+            _flat(context_lens, "context_lens", torch.int32, (S,)))
+    maxb = int(block_tables.shape[1])
+    if max_context_len is None:
+        max_context_len = maxb * B
+    if workspace is None:
+        workspace = alloc_workspace(S, Hq, Hkv, D, B, max_context_len, q.device)
+        if stream is not None:   # allocated on the current stream, used on another
+            workspace.record_stream(stream)
+    st = lib().pa_paged_decode_attention_fp8(
+        *args, float(scale), Hkv, S, Hq, D, B, maxb, int(max_context_len), NB, code,
+        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+        _stream(stream))
+    _check(st, "pa_paged_decode_attention_fp8")
+    return out
+
+
+def pa_copy_blocks_fp8(k_cache, v_cache, kv_scale, block_mapping, stream=None):
+    """pa_copy_blocks on the 8-bit pool: codes and scales of every (src, dst) row."""
+    torch = _torch()
+    _here(k_cache=k_cache, v_cache=v_cache, kv_scale=kv_scale, block_mapping=block_mapping)
+    pool = _pool_fp8(k_cache, v_cache, kv_scale)
+    NB, Hkv, B, D = k_cache.shape
+    pairs = _flat(block_mapping, "block_mapping", torch.int64, (None, 2))
+    st = lib().pa_copy_blocks_fp8(*pool, pairs, int(block_mapping.shape[0]), Hkv, D, B, NB,
+                                  _stream(stream))
+    _check(st, "pa_copy_blocks_fp8")
+
+
+def pa_gather_cache_fp8(key, value, k_cache, v_cache, kv_scale, block_tables, key_start,
+                        stream=None):
+    """Cached rows out of the 8-bit pool: rows key_start[s] .. key_start[s+1]-1 of key and value
+    [T, Hkv, D] (16 bits) become positions 0, 1, ... of sequence s; later rows are left."""
+    torch = _torch()
+    _here(key=key, value=value, k_cache=k_cache, v_cache=v_cache, kv_scale=kv_scale,
+          block_tables=block_tables, key_start=key_start)
+    pool = _pool_fp8(k_cache, v_cache, kv_scale)
+    NB, Hkv, B, D = k_cache.shape
+    code = _dtype_code(key)
+    S = max(0, key_start.shape[0] - 1) if key_start.dim() == 1 else 0
+    T = key.shape[0]
+    st = lib().pa_gather_cache_fp8(
+        _flat(key, "key", key.dtype, (T, Hkv, D)), _flat(value, "value", key.dtype, (T, Hkv, D)),
+        *pool, _flat(block_tables, "block_tables", torch.int32, (S, None)),
+        _flat(key_start, "key_start", torch.int32, (S + 1,)), S, T, Hkv, D, B,
+        int(block_tables.shape[1]), NB, code, _stream(stream))
+    _check(st, "pa_gather_cache_fp8")
 
 
 # --------------------------------------------------------------------------- block manager

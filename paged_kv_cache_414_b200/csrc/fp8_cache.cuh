@@ -1,0 +1,343 @@
+// The 8-bit cache's own operators and the rotary cache write, for sm_100a.
+//
+// An 8-bit pool holds e4m3 codes, K and V each [NB, Hkv, B, D] bytes, and one
+// fp32 scale per (block, kv head, K or V, token): kv_scale [NB, Hkv, 2, B].
+// A cached element is code * scale; a row's scale is max(amax, 2^-100) / 448
+// with amax the row's largest magnitude and 448 e4m3's largest value, so a
+// row's largest element keeps e4m3's full 4 significant bits whatever the
+// row's size, and a row of zeros needs no special case.  (One scale per token
+// rather than per block or per pool: writing a token never re-scales another.)
+//
+// All three kernels move bytes: their bound is HBM, or the launch for small
+// calls.
+#pragma once
+
+#include <cuda_fp8.h>
+#include <stdint.h>
+
+#include "pa_device.cuh"
+
+namespace pa {
+
+constexpr float kE4m3Max = 448.f;
+constexpr float kLeastAmax = 7.888609052210118e-31f;   // 2^-100
+
+struct RopeParams {
+  void *q_out;                 // [T, Hq, D], row stride q_out_stride elements
+  const void *q, *k, *v;       // [T, H, D], row strides below
+  void *k_cache, *v_cache;
+  float *kv_scale;             // e4m3 pool only
+  const int64_t *slots;        // [T]
+  const int64_t *positions;    // [axes, T]
+  const float *cos_sin;        // [max_position, rotary]: cosines, then sines
+  long long q_out_stride, q_stride, k_stride, v_stride;
+  long long num_slots;
+  long long units;             // T * head_slots
+  int num_tokens, num_q_heads, num_kv_heads, block_size;
+  int rotary, axes, max_position;
+  int sect[3];                 // frequency pairs before axis 1, 2, 3
+  int head_slots;              // ceil((Hq + 2 Hkv) / heads per thread)
+};
+
+// Rotary positions and the cache write.  Frequency pair j of a head's first
+// `rotary` columns is turned by the angle of the position its axis gives:
+//   a' = a cos - b sin,  b' = b cos + a sin,
+// (a, b) = columns (j, j + rotary/2), or (2j, 2j + 1) with PAIRS.  D/16 lanes
+// share a head row, 16 columns each, chosen so that lane l owns the pairs
+// 8l .. 8l+7 in either order and both its loads and its 16-bit stores are
+// 16-byte vectors; a row's amax is a shuffle among its lanes.  A thread takes
+// HPT heads of one token, `head_slots` apart, so that neighbouring lanes read
+// neighbouring rows and the table's cosines and sines are fetched once for all
+// of them; all its rows are loaded before any is stored.
+template <typename T, int D, bool FP8, bool PAIRS, int HPT>
+__global__ void __launch_bounds__(256) rope_and_cache_kernel(const RopeParams p) {
+  constexpr int LPR = D / 16;
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int l = threadIdx.x % LPR;
+  const long long u = (long long)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+  // lanes past the last unit repeat it without storing: the shuffles below
+  // need whole warps
+  const bool live = u < p.units;
+  const long long uu = live ? u : p.units - 1;
+  const long long t = uu / p.head_slots;
+  const int hs = (int)(uu - t * p.head_slots);
+  const int nq = p.num_q_heads, nk = nq + p.num_kv_heads, nv = nk + p.num_kv_heads;
+
+  // the token's positions, one per axis; a bad one skips the token
+  bool ok = live;
+  long long pos[4];
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    pos[a] = a < p.axes ? p.positions[(long long)a * p.num_tokens + t] : 0;
+    if (a < p.axes && (pos[a] < 0 || pos[a] >= p.max_position)) {
+      if (live && hs == 0 && l == 0) flag_error(PA_DEVERR_POSITION);
+      ok = false;
+      pos[a] = 0;
+    }
+  }
+  const bool turns = 16 * l < p.rotary;
+  const int e0 = PAIRS || !turns ? 16 * l : 8 * l;
+  const int e1 = PAIRS || !turns ? 16 * l + 8 : p.rotary / 2 + 8 * l;
+
+  // this lane's 16 columns of each of its heads
+  uint4 x[HPT][2];
+#pragma unroll
+  for (int i = 0; i < HPT; ++i) {
+    const int h = hs + i * p.head_slots;
+    const T *row = nullptr;
+    if (ok && h < nq) {
+      if (p.q) row = static_cast<const T *>(p.q) + t * p.q_stride + (long long)h * D;
+    } else if (ok && h < nk) {
+      row = static_cast<const T *>(p.k) + t * p.k_stride + (long long)(h - nq) * D;
+    } else if (ok && h < nv) {
+      row = static_cast<const T *>(p.v) + t * p.v_stride + (long long)(h - nk) * D;
+    }
+    x[i][0] = row ? *reinterpret_cast<const uint4 *>(row + e0) : make_uint4(0, 0, 0, 0);
+    x[i][1] = row ? *reinterpret_cast<const uint4 *>(row + e1) : make_uint4(0, 0, 0, 0);
+  }
+  const int64_t slot = p.slots ? p.slots[t] : -1;
+
+  float c[8], s[8];
+  if (turns && hs < nk) {
+    const int j0 = 8 * l;
+    auto axis = [&](int j) {
+      return (j >= p.sect[0] ? 1 : 0) + (j >= p.sect[1] ? 1 : 0) + (j >= p.sect[2] ? 1 : 0);
+    };
+    auto line = [&](int j) {
+      const int a = axis(j);
+      const long long ps = a == 0 ? pos[0] : (a == 1 ? pos[1] : (a == 2 ? pos[2] : pos[3]));
+      return p.cos_sin + ps * p.rotary + j;
+    };
+    if (axis(j0) == axis(j0 + 7)) {
+      const float *f = line(j0);
+#pragma unroll
+      for (int m = 0; m < 8; m += 4) {
+        const float4 fc = __ldg(reinterpret_cast<const float4 *>(f + m));
+        const float4 fs = __ldg(reinterpret_cast<const float4 *>(f + p.rotary / 2 + m));
+        c[m] = fc.x, c[m + 1] = fc.y, c[m + 2] = fc.z, c[m + 3] = fc.w;
+        s[m] = fs.x, s[m + 1] = fs.y, s[m + 2] = fs.z, s[m + 3] = fs.w;
+      }
+    } else {   // a section ends among these pairs
+#pragma unroll
+      for (int m = 0; m < 8; ++m) {
+        const float *f = line(j0 + m);
+        c[m] = __ldg(f);
+        s[m] = __ldg(f + p.rotary / 2);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int m = 0; m < 8; ++m) c[m] = 1.f, s[m] = 0.f;
+  }
+
+  bool keep = ok && slot >= 0;
+  if (slot >= p.num_slots) {
+    if (ok && hs == 0 && l == 0) flag_error(PA_DEVERR_SLOT);
+    keep = false;
+  }
+  const long long blk = keep ? slot / p.block_size : 0;
+  const int off = keep ? (int)(slot - blk * p.block_size) : 0;
+
+#pragma unroll
+  for (int i = 0; i < HPT; ++i) {
+    const int h = hs + i * p.head_slots;
+    const bool is_q = h < nq, is_k = !is_q && h < nk, is_v = !is_q && !is_k && h < nv;
+    float f[16];   // columns e0 .. e0+7, then e1 .. e1+7
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const uint32_t g[4] = {x[i][w].x, x[i][w].y, x[i][w].z, x[i][w].w};
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const float2 v2 = Mma<T>::unpack(g[m]);
+        f[8 * w + 2 * m] = v2.x;
+        f[8 * w + 2 * m + 1] = v2.y;
+      }
+    }
+    if (!is_v && turns) {
+#pragma unroll
+      for (int m = 0; m < 8; ++m) {
+        const int ia = PAIRS ? 2 * m : m, ib = PAIRS ? 2 * m + 1 : m + 8;
+        const float a = f[ia], b = f[ib];
+        f[ia] = a * c[m] - b * s[m];
+        f[ib] = b * c[m] + a * s[m];
+      }
+    }
+    float amax = 0.f;
+    if (FP8) {
+#pragma unroll
+      for (int m = 0; m < 16; ++m) amax = fmaxf(amax, fabsf(f[m]));
+#pragma unroll
+      for (int d = 1; d < LPR; d <<= 1)
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+    }
+    if (is_q || !FP8) {
+      uint4 y[2];
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+        y[w] = make_uint4(Mma<T>::pack(f[8 * w], f[8 * w + 1]),
+                          Mma<T>::pack(f[8 * w + 2], f[8 * w + 3]),
+                          Mma<T>::pack(f[8 * w + 4], f[8 * w + 5]),
+                          Mma<T>::pack(f[8 * w + 6], f[8 * w + 7]));
+      T *row = nullptr;
+      if (is_q) {
+        if (ok && p.q) row = static_cast<T *>(p.q_out) + t * p.q_out_stride + (long long)h * D;
+      } else if (keep && (is_k || is_v)) {
+        row = static_cast<T *>(is_k ? p.k_cache : p.v_cache) +
+              ((blk * p.num_kv_heads + (is_k ? h - nq : h - nk)) * p.block_size + off) * D;
+      }
+      if (row) {
+        *reinterpret_cast<uint4 *>(row + e0) = y[0];
+        *reinterpret_cast<uint4 *>(row + e1) = y[1];
+      }
+    } else if (keep && (is_k || is_v)) {
+      const float top = fmaxf(amax, kLeastAmax);
+      const float inv = kE4m3Max / top;
+      uint32_t w4[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(
+            make_float2(f[4 * m] * inv, f[4 * m + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+        const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(
+            make_float2(f[4 * m + 2] * inv, f[4 * m + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+        w4[m] = (uint32_t)lo | ((uint32_t)hi << 16);
+      }
+      const long long tile = blk * p.num_kv_heads + (is_k ? h - nq : h - nk);
+      uint8_t *row = static_cast<uint8_t *>(is_k ? p.k_cache : p.v_cache) +
+                     (tile * p.block_size + off) * D;
+      *reinterpret_cast<uint2 *>(row + e0) = make_uint2(w4[0], w4[1]);
+      *reinterpret_cast<uint2 *>(row + e1) = make_uint2(w4[2], w4[3]);
+      if (l == 0) p.kv_scale[(tile * 2 + (is_k ? 0 : 1)) * p.block_size + off] = top / kE4m3Max;
+    }
+  }
+}
+
+// Copy-on-write copies of 8-bit blocks: a pair's K codes, V codes and scales
+// are three runs of 16-byte vectors, walked as one; each thread loads all its
+// vectors before it stores any (no destination is also a source).
+constexpr int kCopy8Unroll = 8;
+__global__ void __launch_bounds__(256)
+    copy_blocks_fp8_kernel(uint4 *k_cache, uint4 *v_cache, uint4 *kv_scale,
+                           const int64_t *__restrict__ block_mapping, int code_vec, int scale_vec,
+                           int chunks, int num_blocks) {
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const long long pair = blockIdx.x / chunks;
+  const int chunk = (int)(blockIdx.x - pair * chunks);
+  const int64_t src = __ldg(block_mapping + 2 * pair);
+  const int64_t dst = __ldg(block_mapping + 2 * pair + 1);
+  if (src < 0 || src >= num_blocks || dst < 0 || dst >= num_blocks) {
+    if (chunk == 0 && threadIdx.x == 0) flag_error(PA_DEVERR_COPY_PAIR);
+    return;
+  }
+  const int total = 2 * code_vec + scale_vec;
+  const int beg = chunk * (256 * kCopy8Unroll) + threadIdx.x;
+  auto at = [&](int i, int64_t b) -> uint4 * {
+    if (i < code_vec) return k_cache + b * code_vec + i;
+    if (i < 2 * code_vec) return v_cache + b * code_vec + (i - code_vec);
+    return kv_scale + b * scale_vec + (i - 2 * code_vec);
+  };
+  uint4 r[kCopy8Unroll];
+#pragma unroll
+  for (int k = 0; k < kCopy8Unroll; ++k)
+    if (beg + k * 256 < total) r[k] = *at(beg + k * 256, src);
+#pragma unroll
+  for (int k = 0; k < kCopy8Unroll; ++k)
+    if (beg + k * 256 < total) *at(beg + k * 256, dst) = r[k];
+}
+
+struct GatherParams {
+  void *key, *value;            // [T, Hkv, D]
+  const uint8_t *k_cache, *v_cache;
+  const float *kv_scale;
+  const int32_t *block_tables;  // [S, max_blocks]
+  const int32_t *key_start;     // [S + 1]
+  int num_seqs, num_tokens, num_kv_heads, block_size, max_blocks, num_blocks;
+};
+
+// Cached rows out of the 8-bit pool, packed and in 16 bits (each code * scale
+// is rounded once, to nearest).  A CTA takes kGatherRows output rows: its
+// first row's sequence is the number of sequences that end at or before it,
+// counted by all threads at once (one load deep, no search), the others
+// follow from it; then K and V of every head, in an order that reads a
+// block's tokens of one head one after the other.  gridDim.y splits the
+// heads.  Rows behind the last sequence are left as they are.
+constexpr int kGatherRows = 16;
+template <typename T, int D>
+__global__ void __launch_bounds__(256) gather_cache_fp8_kernel(const GatherParams p) {
+  constexpr int LPR = D / 16;   // lanes of a row, 16 codes each
+  constexpr int UNR = 4;
+  __shared__ long long cell[kGatherRows];   // (block * Hkv * B + offset), or -1
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int r0 = blockIdx.x * kGatherRows;
+  int s0 = 0;
+  for (int i0 = 0; i0 < p.num_seqs; i0 += 256) {
+    const int i = i0 + threadIdx.x;
+    s0 += __syncthreads_count(i < p.num_seqs && __ldg(p.key_start + i + 1) <= r0);
+  }
+  if (threadIdx.x < kGatherRows) {
+    const int r = r0 + threadIdx.x;
+    int s = s0;
+    while (s < p.num_seqs && __ldg(p.key_start + s + 1) <= r) ++s;
+    long long c = -1;
+    if (r < p.num_tokens && s < p.num_seqs) {
+      const long long pos = (long long)r - __ldg(p.key_start + s);
+      if (pos < 0 || pos >= (long long)p.max_blocks * p.block_size) {
+        flag_error(PA_DEVERR_CONTEXT_LEN);
+      } else {
+        const int blk = __ldg(p.block_tables + (long long)s * p.max_blocks + pos / p.block_size);
+        if (blk < 0 || blk >= p.num_blocks)
+          flag_error(PA_DEVERR_BLOCK_ID);
+        else
+          c = (long long)blk * p.num_kv_heads * p.block_size + pos % p.block_size;
+      }
+    }
+    cell[threadIdx.x] = c;
+  }
+  __syncthreads();
+  const int B = p.block_size;
+  const int rows = 2 * p.num_kv_heads * kGatherRows;        // K rows of every head, then V rows
+  const int step = gridDim.y * (256 / LPR);
+  const int l = threadIdx.x % LPR;
+  for (int base = blockIdx.y * (256 / LPR) + threadIdx.x / LPR; base < rows; base += UNR * step) {
+    uint4 w[UNR];
+    float sc[UNR];
+#pragma unroll
+    for (int k = 0; k < UNR; ++k) {
+      const int i = base + k * step;
+      const int row = i % kGatherRows, hv = i / kGatherRows;   // hv: (K or V, head)
+      const long long c = i < rows ? cell[row] : -1;
+      if (c >= 0) {
+        const int isv = hv >= p.num_kv_heads, h = isv ? hv - p.num_kv_heads : hv;
+        const long long tok = c + (long long)h * B;            // row of the code pool
+        w[k] = __ldg(reinterpret_cast<const uint4 *>((isv ? p.v_cache : p.k_cache) + tok * D) + l);
+        // scale [blk, h, isv, off]: tile = (tok / B), off = tok % B
+        const long long tile = tok / B;
+        sc[k] = __ldg(p.kv_scale + (tile * 2 + isv) * B + (tok - tile * B));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < UNR; ++k) {
+      const int i = base + k * step;
+      const int row = i % kGatherRows, hv = i / kGatherRows;
+      if (i >= rows || cell[row] < 0) continue;
+      const int isv = hv >= p.num_kv_heads, h = isv ? hv - p.num_kv_heads : hv;
+      const uint32_t g[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+      uint32_t y[8];
+#pragma unroll
+      for (int m = 0; m < 8; ++m) {
+        const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
+            (__nv_fp8x2_storage_t)(g[m >> 1] >> (16 * (m & 1))), __NV_E4M3);
+        const float2 f = __half22float2(__half2(hr));
+        y[m] = Mma<T>::pack(f.x * sc[k], f.y * sc[k]);
+      }
+      T *dst = static_cast<T *>(isv ? p.value : p.key) +
+               ((long long)(r0 + row) * p.num_kv_heads + h) * D + 16 * l;
+      reinterpret_cast<uint4 *>(dst)[0] = make_uint4(y[0], y[1], y[2], y[3]);
+      reinterpret_cast<uint4 *>(dst)[1] = make_uint4(y[4], y[5], y[6], y[7]);
+    }
+  }
+}
+
+}  // namespace pa

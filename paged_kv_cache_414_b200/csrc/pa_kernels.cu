@@ -15,6 +15,8 @@
 #include "cache_ops.cuh"
 #include "decode_attention.cuh"
 #include "prefill_attention.cuh"
+#include "fp8_cache.cuh"
+#include "decode_fp8.cuh"
 
 namespace {
 
@@ -566,3 +568,6 @@ int pa_decode_tuning(int nstage, int ctas_per_sm, int min_tiles_per_warp) {
 }
 
 }  // extern "C"
+
+// Operators around the 8-bit cache and the prompt pass.
+#include "serving_api.cuh"

@@ -1,0 +1,382 @@
+// C entry points around the 8-bit paged cache: rotary positions with the cache
+// write, decode attention, gather and block copies.  Included at the end of
+// pa_kernels.cu, whose helpers (tensor-map encoder, argument checks, wait
+// limit) it uses.
+#pragma once
+
+namespace {
+
+bool aligned_stride(long long elements, int head_dim, int heads) {
+  return elements >= (long long)heads * head_dim && elements % 8 == 0;
+}
+
+// Launch with programmatic stream serialisation: the grid may be scheduled
+// while the kernel before it on the stream finishes, and waits for it before
+// its first global access.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem,
+                             cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
+}
+
+// ---------------------------------------------------------------- rotary cache write
+
+template <typename T, int D, bool FP8, bool PAIRS>
+int launch_rope(pa::RopeParams &p, cudaStream_t stream) {
+  constexpr int LPR = D / 16;
+  const int heads = p.num_q_heads + 2 * p.num_kv_heads;
+  // One head per thread while the call is too small to fill the GPU, four
+  // (which share the table's row) once it is not.
+  const bool many = (long long)p.num_tokens * heads * LPR >= 148ll * 2048 * 4;
+  const int hpt = many ? 4 : 1;
+  p.head_slots = (heads + hpt - 1) / hpt;
+  p.units = (long long)p.num_tokens * p.head_slots;
+  const long long blocks = (p.units + 256 / LPR - 1) / (256 / LPR);
+  if (blocks >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+  const cudaError_t e =
+      many ? launch_dependent(pa::rope_and_cache_kernel<T, D, FP8, PAIRS, 4>, dim3((unsigned)blocks),
+                              256, 0, stream, p)
+           : launch_dependent(pa::rope_and_cache_kernel<T, D, FP8, PAIRS, 1>, dim3((unsigned)blocks),
+                              256, 0, stream, p);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+template <typename T, int D>
+int dispatch_rope(pa::RopeParams &p, bool fp8, bool pairs, cudaStream_t stream) {
+  if (fp8)
+    return pairs ? launch_rope<T, D, true, true>(p, stream)
+                 : launch_rope<T, D, true, false>(p, stream);
+  return pairs ? launch_rope<T, D, false, true>(p, stream)
+               : launch_rope<T, D, false, false>(p, stream);
+}
+
+int rope_and_cache(bool fp8, void *q_out, const void *q, const void *key, const void *value,
+                   void *k_cache, void *v_cache, float *kv_scale, const int64_t *slot_mapping,
+                   const int64_t *positions, const float *cos_sin, const int *sections,
+                   int num_axes, int rotary_dim, int max_position, int interleaved,
+                   long long q_out_stride, long long q_stride, long long key_stride,
+                   long long value_stride, int num_tokens, int num_q_heads, int num_kv_heads,
+                   int head_dim, int block_size, int num_blocks, pa_dtype dtype,
+                   cudaStream_t stream) {
+  if (num_tokens < 0 || num_q_heads < 0 || num_kv_heads <= 0 || num_blocks < 0 || head_dim <= 0 ||
+      block_size <= 0 || rotary_dim < 0 || rotary_dim > head_dim)
+    return PA_ERR_ARG;
+  if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_ARG;
+  if (!supported_shape(head_dim, block_size)) return PA_ERR_UNSUPPORTED;
+  if (rotary_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
+  int bound[3] = {1 << 30, 1 << 30, 1 << 30};   // pairs before axis 1, 2, 3
+  if (rotary_dim > 0) {
+    if (num_axes < 1 || num_axes > 4) return PA_ERR_UNSUPPORTED;
+    if (max_position <= 0 || !sections) return PA_ERR_ARG;
+    int sum = 0;
+    for (int a = 0; a < num_axes; ++a) {
+      if (sections[a] < 0 || sections[a] > rotary_dim / 2) return PA_ERR_ARG;
+      if (a > 0) bound[a - 1] = sum;
+      sum += sections[a];
+    }
+    if (sum != rotary_dim / 2) return PA_ERR_ARG;
+  }
+  if (num_tokens == 0) return PA_OK;
+  const int q_heads = q ? num_q_heads : 0;
+  if (!key || !value || !k_cache || !v_cache || !slot_mapping || (fp8 && !kv_scale) ||
+      (rotary_dim > 0 && (!positions || !cos_sin)) || (q && !q_out) || (q && num_q_heads == 0))
+    return PA_ERR_ARG;
+  if (!aligned(key, 16) || !aligned(value, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(slot_mapping, 8) || !aligned(q, 16) || !aligned(q_out, 16) ||
+      !aligned(kv_scale, 16) || !aligned(positions, 8) || !aligned(cos_sin, 16))
+    return PA_ERR_ARG;
+  if (!aligned_stride(key_stride, head_dim, num_kv_heads) ||
+      !aligned_stride(value_stride, head_dim, num_kv_heads) ||
+      (q && (!aligned_stride(q_stride, head_dim, num_q_heads) ||
+             !aligned_stride(q_out_stride, head_dim, num_q_heads))))
+    return PA_ERR_ARG;
+  pa::RopeParams p;
+  p.q_out = q_out;
+  p.q = q;
+  p.k = key;
+  p.v = value;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.kv_scale = kv_scale;
+  p.slots = slot_mapping;
+  p.positions = positions;
+  p.cos_sin = cos_sin;
+  p.q_out_stride = q_out_stride;
+  p.q_stride = q_stride;
+  p.k_stride = key_stride;
+  p.v_stride = value_stride;
+  p.num_slots = (long long)num_blocks * block_size;
+  p.num_tokens = num_tokens;
+  p.num_q_heads = q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.block_size = block_size;
+  p.rotary = rotary_dim;
+  p.axes = rotary_dim > 0 ? num_axes : 0;
+  p.max_position = max_position;
+  for (int a = 0; a < 3; ++a) p.sect[a] = bound[a];
+  if (dtype == PA_BF16)
+    return head_dim == 128 ? dispatch_rope<__nv_bfloat16, 128>(p, fp8, interleaved != 0, stream)
+                           : dispatch_rope<__nv_bfloat16, 64>(p, fp8, interleaved != 0, stream);
+  return head_dim == 128 ? dispatch_rope<__half, 128>(p, fp8, interleaved != 0, stream)
+                         : dispatch_rope<__half, 64>(p, fp8, interleaved != 0, stream);
+}
+
+// ---------------------------------------------------------------- 8-bit decode
+
+// The code pool as rows of D bytes; a box is one (block, kv head) tile, with
+// the swizzle as wide as a row.
+bool encode_code_map(CUtensorMap *m, const void *base, long long rows, int D, int B) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)D};
+  cuuint32_t box[2] = {(cuuint32_t)D, (cuuint32_t)B};
+  cuuint32_t estr[2] = {1u, 1u};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int NT>
+int launch_decode_fp8(pa::DecodeFp8Params &p, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                      uint8_t *workspace, size_t workspace_bytes, int dev, int sms,
+                      cudaStream_t stream) {
+  auto kern = pa::paged_decode_fp8_kernel<D, NT, kWarpsPerCta>;
+  const int G = p.d.group;
+  const size_t per_stage = (size_t)kWarpsPerCta * (pa::fp8_stage_bytes(D) + pa::kF8ScaleBytes +
+                                                   (size_t)G * D * 2 + sizeof(pa::Fp8Tile) +
+                                                   sizeof(uint64_t));
+  int ctas = NT == 1 ? 3 : 2;
+  const size_t budget = 228 * 1024;
+  auto stages_for = [&](int c) { return (int)((budget / c - 2304) / per_stage); };
+  int nst = std::min(stages_for(ctas), 4);
+  if (const int want = g_tune_ctas.load()) ctas = std::min(want, NT == 1 ? 3 : 2);
+  nst = std::min(stages_for(ctas), 4);
+  if (const int want = g_tune_nstage.load()) nst = std::min(stages_for(ctas), want);
+  nst = std::max(nst, 1);
+  const size_t smem = 1024 + per_stage * nst;
+  static std::atomic<size_t> attr_set[kMaxDevices];
+  if (attr_set[dev].load() < smem) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+        cudaSuccess)
+      return PA_ERR_CUDA;
+    attr_set[dev].store(smem);
+  }
+  const int grid = sms * ctas, w_total = grid * kWarpsPerCta;
+  size_t off_ml, off_o;
+  if (workspace_bytes < workspace_for(w_total, G, D, &off_ml, &off_o)) return PA_ERR_WORKSPACE;
+  p.d.meta = reinterpret_cast<long long *>(workspace);
+  p.d.part_ml = reinterpret_cast<float *>(workspace + off_ml);
+  p.d.part_o = reinterpret_cast<float *>(workspace + off_o);
+  p.d.nstage = nst;
+  const int mt = g_tune_min_tiles.load();
+  p.d.min_tiles = mt > 0 ? mt : 4;
+  if (launch_dependent(kern, dim3(grid), kWarpsPerCta * 32, smem, stream, kmap, vmap, p) !=
+      cudaSuccess)
+    return PA_ERR_CUDA;
+  // the split merge of the 16-bit kernel: one warp per boundary and head group
+  cudaError_t e;
+  if (G <= 4) {
+    e = launch_dependent(pa::paged_decode_merge_kernel<D, 4>, dim3((w_total - 1 + 3) / 4), 128, 0,
+                         stream, p.d, w_total, 1);
+  } else {
+    const int hc = (G + 1) / 2;
+    e = launch_dependent(pa::paged_decode_merge_kernel<D, 2>,
+                         dim3((unsigned)(((long long)(w_total - 1) * hc + 3) / 4)), 128, 0, stream,
+                         p.d, w_total, hc);
+  }
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pa_rope_and_cache(void *q_out, const void *q, const void *key, const void *value,
+                      void *k_cache, void *v_cache, const int64_t *slot_mapping,
+                      const int64_t *positions, const float *cos_sin, const int *sections,
+                      int num_axes, int rotary_dim, int max_position, int interleaved,
+                      int64_t q_out_stride, int64_t q_stride, int64_t key_stride,
+                      int64_t value_stride, int num_tokens, int num_q_heads, int num_kv_heads,
+                      int head_dim, int block_size, int num_blocks, pa_dtype dtype,
+                      pa_stream_t stream) {
+  return rope_and_cache(false, q_out, q, key, value, k_cache, v_cache, nullptr, slot_mapping,
+                        positions, cos_sin, sections, num_axes, rotary_dim, max_position,
+                        interleaved, q_out_stride, q_stride, key_stride, value_stride, num_tokens,
+                        num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, dtype,
+                        (cudaStream_t)stream);
+}
+
+int pa_rope_and_cache_fp8(void *q_out, const void *q, const void *key, const void *value,
+                          void *k_cache, void *v_cache, float *kv_scale,
+                          const int64_t *slot_mapping, const int64_t *positions,
+                          const float *cos_sin, const int *sections, int num_axes, int rotary_dim,
+                          int max_position, int interleaved, int64_t q_out_stride,
+                          int64_t q_stride, int64_t key_stride, int64_t value_stride,
+                          int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                          int block_size, int num_blocks, pa_dtype dtype, pa_stream_t stream) {
+  return rope_and_cache(true, q_out, q, key, value, k_cache, v_cache, kv_scale, slot_mapping,
+                        positions, cos_sin, sections, num_axes, rotary_dim, max_position,
+                        interleaved, q_out_stride, q_stride, key_stride, value_stride, num_tokens,
+                        num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, dtype,
+                        (cudaStream_t)stream);
+}
+
+int pa_paged_decode_attention_fp8(float *out, const void *q, const void *k_cache,
+                                  const void *v_cache, const float *kv_scale,
+                                  const int32_t *block_tables, const int32_t *context_lens,
+                                  float scale, int num_kv_heads, int num_seqs, int num_q_heads,
+                                  int head_dim, int block_size, int max_blocks_per_seq,
+                                  int max_context_len, int num_blocks, pa_dtype dtype,
+                                  void *workspace, size_t workspace_bytes, pa_stream_t stream) {
+  if (num_seqs < 0 || num_kv_heads <= 0 || num_q_heads <= 0 || head_dim <= 0 || block_size <= 0)
+    return PA_ERR_ARG;
+  if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_ARG;
+  if (num_q_heads % num_kv_heads != 0) return PA_ERR_ARG;
+  if (!supported_shape(head_dim, block_size) || num_q_heads / num_kv_heads > 16)
+    return PA_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return PA_OK;
+  if (max_blocks_per_seq <= 0 || num_blocks <= 0 || max_context_len < 0 ||
+      (long long)max_context_len > (long long)max_blocks_per_seq * block_size)
+    return PA_ERR_ARG;
+  if ((long long)num_blocks * num_kv_heads * block_size >= (1ll << 31) ||
+      (long long)max_blocks_per_seq * block_size >= (1ll << 30))
+    return PA_ERR_UNSUPPORTED;
+  if (!out || !q || !k_cache || !v_cache || !kv_scale || !block_tables || !context_lens)
+    return PA_ERR_ARG;
+  if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(kv_scale, 16) || !aligned(block_tables, 4) || !aligned(context_lens, 4))
+    return PA_ERR_ARG;
+  if (!workspace || !aligned(workspace, 256)) return PA_ERR_WORKSPACE;
+  int dev;
+  if (current_device(&dev) != PA_OK || dev >= kMaxDevices) return PA_ERR_CUDA;
+  const int sms = sm_count(dev);
+  if (sms <= 0) return PA_ERR_CUDA;
+  CUtensorMap kmap, vmap;
+  const long long rows = (long long)num_blocks * num_kv_heads * block_size;
+  if (!encode_code_map(&kmap, k_cache, rows, head_dim, block_size) ||
+      !encode_code_map(&vmap, v_cache, rows, head_dim, block_size))
+    return PA_ERR_CUDA;
+  pa::DecodeFp8Params p = {};
+  p.d.out = out;
+  p.d.q = static_cast<const uint8_t *>(q);
+  p.d.block_tables = block_tables;
+  p.d.context_lens = context_lens;
+  p.d.scale_log2 = scale * 1.4426950408889634f;
+  p.d.num_seqs = num_seqs;
+  p.d.num_q_heads = num_q_heads;
+  p.d.num_kv_heads = num_kv_heads;
+  p.d.group = num_q_heads / num_kv_heads;
+  p.d.head_dim = head_dim;
+  p.d.max_blocks = (int)(((long long)max_blocks_per_seq * block_size + pa::kF8Tile - 1) /
+                         pa::kF8Tile);
+  p.d.num_blocks = num_blocks;
+  p.d.wait_ns = g_wait_limit_ns.load();
+  p.kv_scale = kv_scale;
+  p.table_blocks = max_blocks_per_seq;
+  p.block_size = block_size;
+  p.q_bf16 = dtype == PA_BF16;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  cudaStream_t st = (cudaStream_t)stream;
+  const bool wide = p.d.group > 8;
+  if (head_dim == 128)
+    return wide ? launch_decode_fp8<128, 2>(p, kmap, vmap, ws, workspace_bytes, dev, sms, st)
+                : launch_decode_fp8<128, 1>(p, kmap, vmap, ws, workspace_bytes, dev, sms, st);
+  return wide ? launch_decode_fp8<64, 2>(p, kmap, vmap, ws, workspace_bytes, dev, sms, st)
+              : launch_decode_fp8<64, 1>(p, kmap, vmap, ws, workspace_bytes, dev, sms, st);
+}
+
+int pa_copy_blocks_fp8(void *k_cache, void *v_cache, float *kv_scale, const int64_t *block_mapping,
+                       int num_pairs, int num_kv_heads, int head_dim, int block_size,
+                       int num_blocks, pa_stream_t stream) {
+  if (num_pairs < 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || num_blocks < 0)
+    return PA_ERR_ARG;
+  if (!supported_shape(head_dim, block_size)) return PA_ERR_UNSUPPORTED;
+  if (num_pairs == 0) return PA_OK;
+  if (!k_cache || !v_cache || !kv_scale || !block_mapping) return PA_ERR_ARG;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(kv_scale, 16) ||
+      !aligned(block_mapping, 8))
+    return PA_ERR_ARG;
+  const long long code_vec = (long long)num_kv_heads * block_size * head_dim / 16;
+  const long long scale_vec = (long long)num_kv_heads * 2 * block_size / 4;
+  const long long per_cta = 256ll * pa::kCopy8Unroll;
+  const long long chunks = (2 * code_vec + scale_vec + per_cta - 1) / per_cta;
+  if (code_vec >= (1ll << 28) || chunks * num_pairs >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+  const cudaError_t e = launch_dependent(
+      pa::copy_blocks_fp8_kernel, dim3((unsigned)(chunks * num_pairs)), 256, 0,
+      (cudaStream_t)stream, static_cast<uint4 *>(k_cache), static_cast<uint4 *>(v_cache),
+      reinterpret_cast<uint4 *>(kv_scale), block_mapping, (int)code_vec, (int)scale_vec,
+      (int)chunks, num_blocks);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+int pa_gather_cache_fp8(void *key, void *value, const void *k_cache, const void *v_cache,
+                        const float *kv_scale, const int32_t *block_tables,
+                        const int32_t *key_start, int num_seqs, int num_tokens, int num_kv_heads,
+                        int head_dim, int block_size, int max_blocks_per_seq, int num_blocks,
+                        pa_dtype dtype, pa_stream_t stream) {
+  if (num_seqs < 0 || num_tokens < 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0)
+    return PA_ERR_ARG;
+  if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_ARG;
+  if (!supported_shape(head_dim, block_size)) return PA_ERR_UNSUPPORTED;
+  if (num_seqs == 0 || num_tokens == 0) return PA_OK;
+  if (max_blocks_per_seq <= 0 || num_blocks <= 0) return PA_ERR_ARG;
+  if (num_kv_heads >= (1 << 20) || num_tokens >= (1 << 31) - pa::kGatherRows)
+    return PA_ERR_UNSUPPORTED;
+  if (!key || !value || !k_cache || !v_cache || !kv_scale || !block_tables || !key_start)
+    return PA_ERR_ARG;
+  if (!aligned(key, 16) || !aligned(value, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(kv_scale, 16) || !aligned(block_tables, 4) || !aligned(key_start, 4))
+    return PA_ERR_ARG;
+  int dev;
+  if (current_device(&dev) != PA_OK || dev >= kMaxDevices) return PA_ERR_CUDA;
+  const int sms = sm_count(dev);
+  if (sms <= 0) return PA_ERR_CUDA;
+  pa::GatherParams p;
+  p.key = key;
+  p.value = value;
+  p.k_cache = static_cast<const uint8_t *>(k_cache);
+  p.v_cache = static_cast<const uint8_t *>(v_cache);
+  p.kv_scale = kv_scale;
+  p.block_tables = block_tables;
+  p.key_start = key_start;
+  p.num_seqs = num_seqs;
+  p.num_tokens = num_tokens;
+  p.num_kv_heads = num_kv_heads;
+  p.block_size = block_size;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_blocks = num_blocks;
+  // Few rows: split the heads over gridDim.y until the grid fills the SMs, a
+  // CTA keeping at least one row per lane group.
+  const int chunks = (num_tokens + pa::kGatherRows - 1) / pa::kGatherRows;
+  const int rows = 2 * num_kv_heads * pa::kGatherRows, groups = 256 / (head_dim / 16);
+  const int most = (rows + groups - 1) / groups;
+  const int split = std::max(1, std::min(most, 8 * sms / chunks));
+  const dim3 grid(chunks, std::min(split, 65535));
+  cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e;
+  if (dtype == PA_BF16)
+    e = head_dim == 128
+            ? launch_dependent(pa::gather_cache_fp8_kernel<__nv_bfloat16, 128>, grid, 256, 0, st, p)
+            : launch_dependent(pa::gather_cache_fp8_kernel<__nv_bfloat16, 64>, grid, 256, 0, st, p);
+  else
+    e = head_dim == 128
+            ? launch_dependent(pa::gather_cache_fp8_kernel<__half, 128>, grid, 256, 0, st, p)
+            : launch_dependent(pa::gather_cache_fp8_kernel<__half, 64>, grid, 256, 0, st, p);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // extern "C"
