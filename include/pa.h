@@ -426,6 +426,44 @@ int pa_gather_cache_fp8(void *key, void *value, const void *k_cache, const void 
                         pa_dtype dtype, pa_stream_t stream);
 
 /*
+ * Causal attention over packed prompts, K and V straight from the projections
+ * (or from pa_gather_cache_fp8): sequence s holds query rows query_start[s] ..
+ * query_start[s+1]-1 and key rows key_start[s] .. key_start[s+1]-1.  With C
+ * queries and L keys, query i stands at position L - C + i and sees the keys
+ * 0 .. L - C + i:
+ *   out[t, h] = softmax(scale * q[t, h] K^T) V
+ * (query head h with kv head h / (num_q_heads / num_kv_heads)).  L > C is a
+ * chunk behind a cached prefix; a query before the first key (C > L) gives
+ * zeros.  fp32 scores, softmax statistics and accumulation; the weights are
+ * rounded to dtype before the product with V, the output once.
+ *
+ *   out           dtype [num_tokens, num_q_heads, head_dim] (device, written);
+ *                 rows of no sequence are left as they were
+ *   q             dtype [num_tokens, num_q_heads, head_dim]
+ *   key, value    dtype [num_key_tokens, num_kv_heads, head_dim]
+ *   *_stride      as for pa_rope_and_cache
+ *   query_start, key_start   int32 [num_seqs + 1] (device), non-decreasing.
+ *                 A sequence that leaves the tensors, or has more queries than
+ *                 max_query_len or more keys than max_key_len, is not computed
+ *                 and sets PA_DEVERR_CONTEXT_LEN
+ *   workspace     pa_prompt_attention_workspace_bytes(...) bytes, 256-byte
+ *                 aligned; that is 0 (workspace may be NULL) unless the queries
+ *                 are too few to occupy the GPU and the keys are split
+ * A NaN or infinite V element reaches, besides the queries that see it, those
+ * up to 2 * (128 / group) - 1 tokens before it in its own sequence; other
+ * sequences never.  head_dim 64 or 128, groups up to 16.
+ */
+size_t pa_prompt_attention_workspace_bytes(int num_seqs, int num_tokens, int num_q_heads,
+                                           int num_kv_heads, int head_dim, int max_query_len,
+                                           int max_key_len);
+int pa_prompt_attention(void *out, const void *q, const void *key, const void *value,
+                        const int32_t *query_start, const int32_t *key_start, float scale,
+                        int num_kv_heads, int num_seqs, int num_tokens, int num_key_tokens,
+                        int num_q_heads, int head_dim, int max_query_len, int max_key_len,
+                        int64_t q_stride, int64_t key_stride, int64_t value_stride, pa_dtype dtype,
+                        void *workspace, size_t workspace_bytes, pa_stream_t stream);
+
+/*
  * Read the sticky device error word of the current device into *flags
  * (PA_DEVERR_* bits; may be NULL), clearing it if `clear` is non-zero.
  * Synchronises the device.  Returns PA_OK when no bit is set,

@@ -12,7 +12,7 @@ the fused ``pa_decode_step``, ``pa_paged_prefill_attention`` (chunked prefill),
 ``pa_copy_blocks``, ``pa_device_error``, ``pa_decode_tuning``, ``pa_set_wait_limit``;
 rotary positions with the cache write, ``pa_rope_and_cache``; the 8-bit pool's
 ``pa_rope_and_cache_fp8``, ``pa_paged_decode_attention_fp8``, ``pa_gather_cache_fp8``
-and ``pa_copy_blocks_fp8``; and the host block manager ``BlockManager`` over the ``pa_bm_*`` calls (prefix
+and ``pa_copy_blocks_fp8``; attention over packed prompts, ``pa_prompt_attention``; and the host block manager ``BlockManager`` over the ``pa_bm_*`` calls (prefix
 caching included).
 """
 from __future__ import annotations
@@ -91,6 +91,9 @@ def _declare(L):
         "pa_paged_decode_attention_fp8": (i32, [vp] * 7 + [f32] + [i32] * 9 + [vp, sz, vp]),
         "pa_copy_blocks_fp8": (i32, [vp] * 4 + [i32] * 5 + [vp]),
         "pa_gather_cache_fp8": (i32, [vp] * 7 + [i32] * 8 + [vp]),
+        "pa_prompt_attention_workspace_bytes": (sz, [i32] * 7),
+        "pa_prompt_attention": (i32, [vp] * 6 + [f32] + [i32] * 8 + [i64] * 3
+                                + [i32, vp, sz, vp]),
         "pa_copy_blocks": (i32, [vp, vp, vp, i32, i32, i32, i32, i32, i32, vp]),
         "pa_device_error": (i32, [c.POINTER(c.c_uint), i32]),
         "pa_bm_create": (vp, [i32, i32, P32]),
@@ -522,6 +525,43 @@ def pa_gather_cache_fp8(key, value, k_cache, v_cache, kv_scale, block_tables, ke
         _flat(key_start, "key_start", torch.int32, (S + 1,)), S, T, Hkv, D, B,
         int(block_tables.shape[1]), NB, code, _stream(stream))
     _check(st, "pa_gather_cache_fp8")
+
+
+def pa_prompt_attention(out, q, key, value, query_start, key_start, scale, num_kv_heads,
+                        max_query_len, max_key_len, workspace=None, stream=None):
+    """Causal attention over packed prompts: out[t, h] = softmax(scale * q[t, h] K^T) V over the
+    keys up to the query's position.  Sequence s holds rows query_start[s] .. of q and out
+    [T, Hq, D] and key_start[s] .. of key and value [Tk, Hkv, D] (16 bits, tokens any multiple of
+    8 elements apart); more keys than queries is a chunk behind a cached prefix.  No sequence may
+    have more queries than max_query_len or more keys than max_key_len."""
+    torch = _torch()
+    _here(out=out, q=q, key=key, value=value, query_start=query_start, key_start=key_start,
+          workspace=workspace)
+    if q.dim() != 3 or key.dim() != 3 or key.shape[1] != num_kv_heads:
+        raise ValueError("q / key shapes disagree")
+    T, Hq, D = q.shape
+    Tk, Hkv, _ = key.shape
+    code = _dtype_code(q)
+    qp, qs = _rows(q, "q", q.dtype, (T, Hq, D))
+    k, ks = _rows(key, "key", q.dtype, (Tk, Hkv, D))
+    v, vs = _rows(value, "value", q.dtype, (Tk, Hkv, D))
+    S = max(0, query_start.shape[0] - 1) if query_start.dim() == 1 else 0
+    args = (_flat(out, "out", q.dtype, (T, Hq, D)), qp, k, v,
+            _flat(query_start, "query_start", torch.int32, (S + 1,)),
+            _flat(key_start, "key_start", torch.int32, (S + 1,)))
+    mq, mk = int(max_query_len), int(max_key_len)
+    if workspace is None:
+        need = int(lib().pa_prompt_attention_workspace_bytes(S, T, Hq, Hkv, D, mq, mk))
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            if stream is not None:   # allocated on the current stream, used on another
+                workspace.record_stream(stream)
+    wp, wb = (None, 0) if workspace is None else (
+        workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    st = lib().pa_prompt_attention(*args, float(scale), Hkv, S, T, Tk, Hq, D, mq, mk, qs, ks, vs,
+                                   code, wp, wb, _stream(stream))
+    _check(st, "pa_prompt_attention")
+    return out
 
 
 # --------------------------------------------------------------------------- block manager

@@ -17,6 +17,7 @@
 #include "prefill_attention.cuh"
 #include "fp8_cache.cuh"
 #include "decode_fp8.cuh"
+#include "prompt_attention.cuh"
 
 namespace {
 

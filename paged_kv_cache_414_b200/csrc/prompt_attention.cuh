@@ -1,0 +1,685 @@
+// Causal attention over packed prompts, on the fifth-generation tensor cores
+// (tcgen05, accumulators in tensor memory).  K and V come straight from the
+// projections, packed like the queries; no pool and no block tables.
+//
+// Sequence s has C queries (rows query_start[s] ..) and L keys (rows
+// key_start[s] ..); query i stands at position p = L - C + i and
+//   out = softmax_{t <= p}(scale <q, k_t>) v,   zeros where p < 0.
+//
+// Work unit: (sequence, pair of query tiles, kv head, piece of the keys).  A
+// query tile is 128 rows = tq = 128 / G tokens x the G heads of one kv head;
+// tiles A and B (2 tq consecutive tokens) share every K/V tile of 128 keys.
+// Units are numbered longest first over all sequences -- found in the kernel
+// by a search over the lengths -- and CTAs, one per SM, take them in that
+// order: the first by blockIdx, the next by cancelling CTAs that have not been
+// launched yet (clusterlaunchcontrol), so that loads, the tensor-memory
+// allocation and the barriers of one unit run on into the next.
+//
+//   warps 0-3   softmax and output of tile A, one thread per row
+//   warps 4-7   the same for tile B
+//   warp 8      TMA producer
+//   warp 9      MMA issue: per K/V tile j, O_A += P_A V_j, S_A(j+1) = Q_A K^T,
+//               then the same for B, so one tile's softmax runs under the
+//               other's MMAs
+//   warp 10     scheduler: finds the next unit one unit ahead
+//   warp 11     zeroes V rows behind the last visible key (they may hold
+//               another sequence's NaN, and 0 x NaN would reach every row)
+//
+// P replaces S in tensor memory, in the inputs' 16-bit type: rounding the
+// weights (2^-9 or 2^-12 each, independent) costs about as much as rounding
+// the output does.  Maximum, sum and O are fp32.  O is rescaled only when a
+// row's maximum grows by more than 2^8 (weights then stay below 2^8).
+#pragma once
+
+#include "prefill_attention.cuh"
+
+namespace pa {
+
+struct PromptParams {
+  void *out;                   // [T, Hq, D]
+  const int32_t *query_start;  // [S + 1]
+  const int32_t *key_start;    // [S + 1]
+  float *part_o;               // [units][pieces][256][D], keys split only
+  float2 *part_ml;             // [units][pieces][256]  (max in log2 units, sum)
+  float scale_log2;            // scale * log2(e)
+  int num_seqs, num_tokens, num_key_tokens, num_q_heads, num_kv_heads, group;
+  int tq;                      // tokens per query tile
+  int max_query, max_key;
+  int pieces;                  // pieces of the keys in the grid
+  int piece_tiles;             // K/V tiles per piece
+  uint64_t wait_ns;
+};
+
+constexpr int kPrRows = 128;
+constexpr int kPrKeys = 128;
+constexpr int kPrThreads = 384;
+constexpr int kPrSeqCache = 256;   // sequences whose (first key, units) a CTA keeps
+constexpr int kPrConsumers = 11;   // warps that read a unit's description
+
+// A unit as the scheduler describes it.
+struct PromptUnit {
+  int n[2];        // K/V tiles of query tiles A and B in this piece; n[0] < 0: no more units
+  int first_key;   // global row of the piece's first key
+  int token0;      // global row of tile A's first token
+  int tokens;      // of tiles A and B
+  int pos0;        // position of tile A's first token, less that of the piece's first key
+  int kv_head;
+  int slot;        // index of its partials
+};
+
+template <int D>
+struct PromptSmem {
+  static constexpr int NCH = D / 64;
+  static constexpr int STAGES = D == 128 ? 2 : 4;
+  static constexpr int REGION = kPrRows * 128;
+  static constexpr int Q_TILE = NCH * REGION;
+  static constexpr int KV_BYTES = NCH * kPrKeys * 128;
+  static constexpr int OFF_K = 2 * Q_TILE;
+  static constexpr int OFF_V = OFF_K + STAGES * KV_BYTES;
+  static constexpr int OFF_BAR = OFF_V + STAGES * KV_BYTES;
+  static constexpr int BYTES = OFF_BAR + 1024;   // the slack aligns the base
+};
+
+// ---------------------------------------------------------------- units
+
+// What the numbering needs of a sequence: units are its pairs of query tiles,
+// pair i has order e0 + i, which grows with the keys it sees.
+__device__ __forceinline__ int2 prompt_seq(const PromptParams &p, int s, bool report) {
+  const int q0 = __ldg(p.query_start + s), q1 = __ldg(p.query_start + s + 1);
+  const int k0 = __ldg(p.key_start + s), k1 = __ldg(p.key_start + s + 1);
+  if (q0 < 0 || q1 < q0 || q1 > p.num_tokens || k0 < 0 || k1 < k0 || k1 > p.num_key_tokens ||
+      q1 - q0 > p.max_query || k1 - k0 > p.max_key) {
+    if (report) flag_error(PA_DEVERR_CONTEXT_LEN);
+    return make_int2(0, 0);
+  }
+  const int w = 2 * p.tq;
+  return make_int2(max(0, (k1 - k0) - (q1 - q0)) / w, (q1 - q0 + w - 1) / w);
+}
+
+// Unit number v in order of decreasing length (ties by sequence): its sequence
+// and pair, or false past the last one.  A whole warp; `cache` holds the first
+// kPrSeqCache sequences' prompt_seq.
+__device__ __forceinline__ bool prompt_find(const PromptParams &p, const int2 *cache, int v, int &s,
+                                            int &pair) {
+  const int lane = threadIdx.x & 31;
+  auto seq = [&](int i) {
+    return i < kPrSeqCache ? cache[i] : prompt_seq(p, i, false);
+  };
+  auto at_least = [&](int e) {   // units of order e or more
+    int n = 0;
+    for (int i = lane; i < p.num_seqs; i += 32) {
+      const int2 q = seq(i);
+      n += min(max(q.x + q.y - e, 0), q.y);
+    }
+    return __reduce_add_sync(0xffffffffu, n);
+  };
+  if (v >= at_least(0)) return false;
+  int lo = 0, hi = (p.max_query + p.max_key) / (2 * p.tq) + 2;   // at_least(lo) > v >= at_least(hi)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (at_least(mid) > v) lo = mid; else hi = mid;
+  }
+  int left = v - at_least(hi);
+  for (int i0 = 0; i0 < p.num_seqs; i0 += 32) {
+    const int i = i0 + lane;
+    const int2 q = i < p.num_seqs ? seq(i) : make_int2(0, 0);
+    const bool has = q.x <= lo && lo < q.x + q.y;
+    const unsigned who = __ballot_sync(0xffffffffu, has);
+    const int many = __popc(who);
+    if (left < many) {
+      const unsigned mine = __ballot_sync(
+          0xffffffffu, has && __popc(who & ((1u << lane) - 1u)) == left);
+      const int src = __ffs(mine) - 1;
+      s = i0 + src;
+      pair = lo - __shfl_sync(0xffffffffu, q.x, src);
+      return true;
+    }
+    left -= many;
+  }
+  return false;
+}
+
+// Tiles of 128 keys that the tokens up to position `last` see.
+__device__ __forceinline__ int prompt_tiles(int last) { return last < 0 ? 0 : last / kPrKeys + 1; }
+
+// Tokens and positions of a pair of query tiles.
+struct PromptPair {
+  int token0, tokens, pos0, key0;
+  int tiles[2];   // of A and B over the whole length
+};
+__device__ __forceinline__ PromptPair prompt_pair(const PromptParams &p, int s, int pair) {
+  const int q0 = __ldg(p.query_start + s), C = __ldg(p.query_start + s + 1) - q0;
+  const int k0 = __ldg(p.key_start + s), L = __ldg(p.key_start + s + 1) - k0;
+  PromptPair u;
+  const int t0 = pair * 2 * p.tq;
+  u.token0 = q0 + t0;
+  u.tokens = min(2 * p.tq, C - t0);
+  u.pos0 = L - C + t0;
+  u.key0 = k0;
+  u.tiles[0] = prompt_tiles(u.pos0 + min(p.tq, u.tokens) - 1);
+  u.tiles[1] = u.tokens > p.tq ? prompt_tiles(u.pos0 + u.tokens - 1) : 0;
+  return u;
+}
+
+// ---------------------------------------------------------------- launch control
+
+// Ask for a CTA that has not been launched yet; the answer (16 bytes) lands in
+// `dst` and completes them on `bar`.
+__device__ __forceinline__ void try_cancel(void *dst, uint64_t *bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], "
+      "[%1];" ::"r"(smem_addr(dst)),
+      "r"(smem_addr(bar))
+      : "memory");
+}
+// blockIdx.x of the CTA that was cancelled in this one's favour, or -1.
+__device__ __forceinline__ int cancelled_block(const void *answer) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(ok), "=r"(x)
+      : "r"(smem_addr(answer))
+      : "memory");
+  return ok ? (int)x : -1;
+}
+
+// max(a, b, c), NaN if any is.
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kPrThreads, 1)
+    prompt_attention_kernel(const __grid_constant__ CUtensorMap qmap,
+                            const __grid_constant__ CUtensorMap kmap,
+                            const __grid_constant__ CUtensorMap vmap, const PromptParams p) {
+  using L = PromptSmem<D>;
+  constexpr int NCH = L::NCH, NST = L::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t *sQ = smem, *sK = smem + L::OFF_K, *sV = smem + L::OFF_V;
+
+  __shared__ uint64_t full_k[NST], full_v[NST], empty_k[NST], empty_v[NST];
+  __shared__ uint64_t q_full, q_empty;      // both query tiles: landed, read by their last S
+  __shared__ uint64_t s_full[2], p_full[2], o_done[2];
+  __shared__ uint64_t v_tail, v_clean;      // the last V tile: landed; its tail is zeros
+  __shared__ uint64_t unit_full[2], unit_empty[2];
+  __shared__ uint64_t answer_bar, drain;
+  __shared__ __align__(16) uint4 answer;
+  __shared__ PromptUnit units[2];
+  __shared__ int2 seqs[kPrSeqCache];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  volatile int *abort = &abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.group;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(&full_k[i], 1);
+      mbar_init(&full_v[i], 1);
+      mbar_init(&empty_k[i], 1);
+      mbar_init(&empty_v[i], 1);
+    }
+    mbar_init(&q_full, 1);
+    mbar_init(&q_empty, 1);
+    mbar_init(&v_tail, 1);
+    mbar_init(&v_clean, 32);
+    mbar_init(&answer_bar, 1);
+    mbar_init(&drain, 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_full[x], 4);
+      mbar_init(&o_done[x], 1);
+      mbar_init(&unit_full[x], 1);
+      mbar_init(&unit_empty[x], kPrConsumers);
+    }
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(&tmem_slot, kPfTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  grid_dependency_wait();
+  allow_dependent_launch();
+
+  // every lane waits; the warp goes on only if all of them saw the phase
+  auto wait_all = [&](uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, pf_wait(bar, parity, abort, p.wait_ns));
+  };
+  // the next unit, by its number in this CTA
+  int taken = 0;
+  auto next_unit = [&](PromptUnit &u) {
+    const int b = taken & 1;
+    if (!wait_all(&unit_full[b], (taken >> 1) & 1)) return false;
+    u = units[b];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&unit_empty[b]);
+    ++taken;
+    return u.n[0] >= 0;
+  };
+
+  // The softmax keeps a row's 128 scores in registers: 208 each for its 256
+  // threads, 80 for the others, of the 384 x 168 that the block starts with.
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 10) {
+      // ------------------------------------------------------------ scheduler
+      for (int i = lane; i < min(p.num_seqs, kPrSeqCache); i += 32)
+        seqs[i] = prompt_seq(p, i, blockIdx.x == 0);
+      if (blockIdx.x == 0)
+        for (int i = kPrSeqCache + lane; i < p.num_seqs; i += 32) prompt_seq(p, i, true);
+      __syncwarp();
+      int block = blockIdx.x, made = 0, asked = 0;
+      while (true) {
+        PromptUnit u;
+        u.n[0] = -1;
+        bool give = block < 0;
+        if (block >= 0) {
+          const int piece = block % p.pieces, rest = block / p.pieces;
+          const int kh = rest % p.num_kv_heads, v = rest / p.num_kv_heads;
+          int s, pair;
+          if (prompt_find(p, seqs, v, s, pair)) {
+            const PromptPair w = prompt_pair(p, s, pair);
+            const int j0 = piece * p.piece_tiles;
+            u.n[0] = min(max(w.tiles[0] - j0, 0), p.piece_tiles);
+            u.n[1] = min(max(w.tiles[1] - j0, 0), p.piece_tiles);
+            u.first_key = w.key0 + j0 * kPrKeys;
+            u.token0 = w.token0;
+            u.tokens = w.tokens;
+            u.pos0 = w.pos0 - j0 * kPrKeys;
+            u.kv_head = kh;
+            u.slot = block;
+            give = u.n[0] > 0 || u.n[1] > 0 || p.pieces == 1;   // no keys: rows of zeros
+          }
+        }
+        if (give) {
+          const int b = made & 1;
+          if (made >= 2 && !wait_all(&unit_empty[b], ((made >> 1) - 1) & 1)) break;
+          if (lane == 0) {
+            units[b] = u;
+            mbar_arrive(&unit_full[b]);
+          }
+          ++made;
+        }
+        if (block < 0 || *abort) break;
+        if (lane == 0) {
+          fence_proxy_async_smem();   // the last answer was read before the next is written
+          mbar_arrive_expect_tx(&answer_bar, 16);
+          try_cancel(&answer, &answer_bar);
+        }
+        __syncwarp();
+        if (!wait_all(&answer_bar, asked & 1)) {
+          mbar_wait_bounded(&answer_bar, asked & 1, kPfDrainLimitNs);   // it lands before the CTA exits
+          break;
+        }
+        ++asked;
+        block = cancelled_block(&answer);
+        __syncwarp();
+      }
+    } else if (warp == 8) {
+      // ------------------------------------------------------------ producer
+      if (lane == 0) {
+        prefetch_tensormap(&qmap);
+        prefetch_tensormap(&kmap);
+        prefetch_tensormap(&vmap);
+      }
+      PromptUnit u;
+      int it = 0, loads = 0, vloads = 0, nq = 0;   // K/V tiles, units with a Q
+      bool ok = true;
+      while (ok && next_unit(u)) {
+        const int nm = max(u.n[0], u.n[1]);
+        for (int j = 0; ok && j < nm; ++j, ++it) {
+          const int st = it % NST;
+          const uint32_t free_phase = (it / NST - 1) & 1;
+          if (it >= NST && !(ok = wait_all(&empty_k[st], free_phase))) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&full_k[st], L::KV_BYTES);
+            for (int c = 0; c < NCH; ++c)
+              tma_load_3d(sK + st * L::KV_BYTES + c * kPrKeys * 128, &kmap, c * 64, u.kv_head,
+                          u.first_key + j * kPrKeys, &full_k[st]);
+          }
+          loads = it + 1;
+          if (j == 0) {
+            if (nq > 0 && !(ok = wait_all(&q_empty, (nq - 1) & 1))) break;
+            const bool two = u.tokens > p.tq;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&q_full, (two ? 2 : 1) * NCH * 128 * p.tq * G);
+              for (int c = 0; c < NCH; ++c) {
+                tma_load_3d(sQ + c * L::REGION, &qmap, c * 64, u.kv_head * G, u.token0, &q_full);
+                if (two)
+                  tma_load_3d(sQ + L::Q_TILE + c * L::REGION, &qmap, c * 64, u.kv_head * G,
+                              u.token0 + p.tq, &q_full);
+              }
+            }
+            ++nq;
+          }
+          if (it >= NST && !(ok = wait_all(&empty_v[st], free_phase))) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&full_v[st], L::KV_BYTES);
+            for (int c = 0; c < NCH; ++c)
+              tma_load_3d(sV + st * L::KV_BYTES + c * kPrKeys * 128, &vmap, c * 64, u.kv_head,
+                          u.first_key + j * kPrKeys, &full_v[st]);
+          }
+          vloads = it + 1;
+        }
+      }
+      // copies still in flight must land before the CTA exits
+      if (lane == 0) {
+        for (int j = max(0, loads - NST); j < loads; ++j)
+          mbar_wait_bounded(&full_k[j % NST], (j / NST) & 1, kPfDrainLimitNs);
+        for (int j = max(0, vloads - NST); j < vloads; ++j)
+          mbar_wait_bounded(&full_v[j % NST], (j / NST) & 1, kPfDrainLimitNs);
+        if (nq > 0) mbar_wait_bounded(&q_full, (nq - 1) & 1, kPfDrainLimitNs);
+      }
+    } else if (warp == 9) {
+      // ------------------------------------------------------------ MMA issue
+      constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
+      const uint32_t idS = umma_idesc_f16(kBf, kPrRows, kPrKeys, false, false);
+      const uint32_t idO = umma_idesc_f16(kBf, kPrRows, D, false, true);
+      const uint64_t dQ0 = umma_desc_sw128(smem_addr(sQ), 16, 1024);
+      const uint64_t dK0 = umma_desc_sw128(smem_addr(sK), 16, 1024);
+      const uint64_t dV0 = umma_desc_sw128(smem_addr(sV), kPrKeys * 128, 1024);
+      constexpr uint32_t kStageStep = L::KV_BYTES >> 4, kQStep = L::Q_TILE >> 4;
+      auto issue_s = [&](int x, int st) {       // S_x = Q_x K^T
+        const uint64_t dq = dQ0 + x * kQStep, dk = dK0 + st * kStageStep;
+        const uint32_t d = tmem + x * 256;
+        constexpr uint32_t kRegion = L::REGION >> 4;
+        if constexpr (D == 128)
+          umma_ss_group8<0, 2, 4, 6, kRegion, kRegion + 2, kRegion + 4, kRegion + 6>(d, dq, dk, idS,
+                                                                                      0u);
+        else
+          umma_ss_group4<0, 2, 4, 6>(d, dq, dk, idS, 0u);
+        umma_commit(&s_full[x]);
+      };
+      auto issue_pv = [&](int x, int st, bool first) {   // O_x (+)= P_x V
+        const uint64_t dv = dV0 + st * kStageStep;
+        const uint32_t pj = tmem + x * 256, d = pj + 128;
+        umma_ts_group8<0, 8, 16, 24, 32, 40, 48, 56, 0, 128, 256, 384, 512, 640, 768, 896>(
+            d, pj, dv, idO, first ? 0u : 1u);
+      };
+      PromptUnit u;
+      int it = 0, nq = 0, np[2] = {0, 0}, nclean = 0;
+      bool ok = true;
+      while (ok && next_unit(u)) {
+        const int nm = max(u.n[0], u.n[1]);
+        if (nm == 0) continue;
+        const bool tail = u.pos0 + u.tokens < nm * kPrKeys;   // keys behind the last position
+        ok = wait_all(&q_full, nq & 1) && wait_all(&full_k[it % NST], (it / NST) & 1);
+        if (!ok) break;
+        ++nq;
+        tc_fence_after();
+        for (int x = 0; x < 2; ++x)
+          if (u.n[x] > 0) issue_s(x, it % NST);
+        umma_commit(&empty_k[it % NST]);
+        if (nm == 1) umma_commit(&q_empty);
+        for (int j = 0; ok && j < nm; ++j, ++it) {
+          const int st = it % NST, sn = (it + 1) % NST;
+          const bool more = j + 1 < nm;
+          ok = wait_all(&full_v[st], (it / NST) & 1);
+          if (ok && tail && !more) {
+            if (lane == 0) mbar_arrive(&v_tail);
+            ok = wait_all(&v_clean, nclean++ & 1);
+          }
+          if (ok && more) ok = wait_all(&full_k[sn], ((it + 1) / NST) & 1);
+          if (!ok) break;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (j >= u.n[x]) continue;
+            ok = wait_all(&p_full[x], np[x]++ & 1);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(x, st, j == 0);
+            if (j + 1 == u.n[x]) umma_commit(&o_done[x]);
+            else issue_s(x, sn);
+          }
+          if (!ok) break;
+          umma_commit(&empty_v[st]);
+          if (more) umma_commit(&empty_k[sn]);
+          if (j + 2 == nm) umma_commit(&q_empty);
+        }
+      }
+      umma_commit(&drain);
+      mbar_wait_bounded(&drain, 0, kPfDrainLimitNs);
+    } else {
+      // ------------------------------------------------------------ V tail
+      // (asked by the MMA warp, which reaches the tile in order: a wait on the
+      // tile's own barrier alone could meet an earlier phase of it)
+      PromptUnit u;
+      int it = 0, asked = 0;
+      while (next_unit(u)) {
+        const int nm = max(u.n[0], u.n[1]);
+        it += nm;
+        const int live = u.pos0 + u.tokens - (nm - 1) * kPrKeys;   // rows of the last tile that count
+        if (nm == 0 || live >= kPrKeys) continue;
+        const int st = (it - 1) % NST;
+        if (!wait_all(&v_tail, asked++ & 1) || !wait_all(&full_v[st], ((it - 1) / NST) & 1)) break;
+        uint8_t *v0 = sV + st * L::KV_BYTES;
+        for (int i = live * 8 + lane; i < kPrKeys * 8; i += 32)
+#pragma unroll
+          for (int c = 0; c < NCH; ++c)
+            *reinterpret_cast<uint4 *>(v0 + c * kPrKeys * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();   // read next by the tensor cores (async proxy)
+        mbar_arrive(&v_clean);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax + output
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int x = warp >> 2;                 // query tile
+    const int r = threadIdx.x & 127;         // this thread's row, and lane of tensor memory
+    const int t = r / G, g = r - t * G;
+    const uint32_t tS = tmem + x * 256 + ((uint32_t)((warp & 3) * 32) << 16), tO = tS + 128;
+    const bool pos_scale = p.scale_log2 > 0.f;
+    const float sl2 = pos_scale ? p.scale_log2 : 1.f;   // else the scores are scaled first
+    PromptUnit u;
+    int ns = 0, no = 0;
+    bool ok = true;
+    while (ok && next_unit(u)) {
+      const int n = u.n[x];
+      const bool row_ok = t < p.tq && x * p.tq + t < u.tokens;
+      const int pos = row_ok ? u.pos0 + x * p.tq + t : u.pos0 + u.tokens - 1;
+      const int pos_min = u.pos0 + x * p.tq;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j, ++ns) {
+        ok = wait_all(&s_full[x], ns & 1);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t v[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_load32_async(tS + c * 32, v + c * 32);
+        tmem_load_wait();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_loaded(v + c * 32);
+        const int lim = pos - j * kPrKeys;                     // keys 0 .. lim of the tile count
+        if (!pos_scale) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * p.scale_log2);
+        }
+        if (pos_min < j * kPrKeys + kPrKeys - 1) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i) v[i] = i <= lim ? v[i] : 0xff800000u;   // -inf
+        }
+        float mx[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(v[i]);
+#pragma unroll
+        for (int i = 4; i < 124; i += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mx[k] = fmax3_nan(mx[k], __uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1]));
+        mx[0] = fmax3_nan(mx[0], __uint_as_float(v[124]), __uint_as_float(v[125]));
+        mx[1] = fmax3_nan(mx[1], __uint_as_float(v[126]), __uint_as_float(v[127]));
+        const float mt = fmax3_nan(fmax3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]) * sl2;
+        // The reference moves only when the maximum has grown by more than 8
+        // (log2 units); the negation takes a NaN along, and the row ends as NaN.
+        const bool bump = !(mt <= m + 8.f);
+        const float m_new = bump ? mt : m;
+        const float ref = m_new == -INFINITY ? 0.f : m_new;    // nothing seen: weights of 0
+        const float alpha = bump ? fast_exp2(m - ref) : 1.f;
+        m = m_new;
+        // O is stable: S(j) was committed after P.V(j-1)
+        if (j > 0 && __any_sync(0xffffffffu, bump)) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 8) {
+            uint32_t o[8];
+            tmem_load8(tO + c, o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_store8(tO + c, o);
+          }
+        }
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t h[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int k = c * 32 + 2 * i;
+            float x0, x1;
+            ffma2(x0, x1, __uint_as_float(v[k]), __uint_as_float(v[k + 1]), sl2, sl2, -ref, -ref);
+            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+            fadd2(sum[(i & 1) * 2], sum[(i & 1) * 2 + 1], sum[(i & 1) * 2], sum[(i & 1) * 2 + 1], p0,
+                  p1);
+            h[i] = Mma<T>::pack(p0, p1);
+          }
+          tmem_store16_async(tS + c * 16, h);
+        }
+        l = l * alpha + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+        tmem_store_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[x]);
+      }
+      if (!ok) break;
+      if (n > 0) {
+        ok = wait_all(&o_done[x], no++ & 1);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      if (p.pieces > 1) {
+        if (n > 0) {      // fp32 partial, as it is, with its maximum and sum
+          const long long row = (long long)u.slot * 256 + x * 128 + r;
+          float *dst = p.part_o + row * D;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            tmem_load16(tO + c, o);
+            if (row_ok)
+#pragma unroll
+              for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<uint4 *>(dst + c + i) =
+                    make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
+          if (row_ok) p.part_ml[row] = make_float2(m, l);
+        }
+      } else {
+        const bool none = l == 0.f;          // nothing seen: zeros, whatever V holds
+        const float inv = 1.f / l;
+        T *dst = static_cast<T *>(p.out) +
+                 ((long long)(u.token0 + x * p.tq + t) * p.num_q_heads + u.kv_head * G + g) * D;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          uint32_t o[16];
+          if (n > 0) tmem_load16(tO + c, o);
+          uint32_t h[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            h[i] = none ? 0u
+                        : Mma<T>::pack(__uint_as_float(o[2 * i]) * inv,
+                                       __uint_as_float(o[2 * i + 1]) * inv);
+          if (row_ok) {
+            *reinterpret_cast<uint4 *>(dst + c) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4 *>(dst + c + 8) = make_uint4(h[4], h[5], h[6], h[7]);
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kPfTmemCols);
+  }
+}
+
+// Join of the pieces of the keys: a CTA takes 32 rows of one (pair of query
+// tiles, kv head), a warp one row at a time, each lane D / 32 columns.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) prompt_join_kernel(const PromptParams p) {
+  constexpr int VPL = D / 32;
+  __shared__ int2 seqs[kPrSeqCache];
+  __shared__ int found[2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int kh = blockIdx.x % p.num_kv_heads, v = blockIdx.x / p.num_kv_heads;
+  if (warp == 0) {
+    for (int i = lane; i < min(p.num_seqs, kPrSeqCache); i += 32) seqs[i] = prompt_seq(p, i, false);
+    __syncwarp();
+    int s = -1, pair = 0;
+    if (!prompt_find(p, seqs, v, s, pair)) s = -1;
+    if (lane == 0) found[0] = s, found[1] = pair;
+  }
+  __syncthreads();
+  if (found[0] < 0) return;
+  const PromptPair u = prompt_pair(p, found[0], found[1]);
+  for (int k = 0; k < 4; ++k) {
+    const int row = blockIdx.y * 32 + warp * 4 + k;   // of the pair's 256
+    const int x = row >> 7, r = row & 127, t = r / p.group, g = r - t * p.group;
+    if (t >= p.tq || x * p.tq + t >= u.tokens) continue;
+    const int n = (u.tiles[x] + p.piece_tiles - 1) / p.piece_tiles;
+    const long long first = ((long long)blockIdx.x * p.pieces) * 256 + row;
+    float M = -INFINITY, den = 0.f, num[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) num[i] = 0.f;
+    for (int i = 0; i < n; ++i) {
+      const float2 ml = __ldcg(p.part_ml + first + (long long)i * 256);
+      const float mn = fmax3_nan(M, ml.x, ml.x);
+      const float ref = mn == -INFINITY ? 0.f : mn;
+      const float a = exp2f(M - ref), b = exp2f(ml.x - ref);
+      const float *src = p.part_o + (first + (long long)i * 256) * D + lane * VPL;
+      den = den * a + ml.y * b;
+      if constexpr (VPL == 4) {
+        const float4 o = __ldcg(reinterpret_cast<const float4 *>(src));
+        num[0] = num[0] * a + o.x * b, num[1] = num[1] * a + o.y * b;
+        num[2] = num[2] * a + o.z * b, num[3] = num[3] * a + o.w * b;
+      } else {
+        const float2 o = __ldcg(reinterpret_cast<const float2 *>(src));
+        num[0] = num[0] * a + o.x * b, num[1] = num[1] * a + o.y * b;
+      }
+      M = mn;
+    }
+    if (den == 0.f) {                 // nothing seen: zeros, whatever V holds
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) num[i] = 0.f;
+      den = 1.f;
+    }
+    const float inv = 1.f / den;
+    T *dst = static_cast<T *>(p.out) +
+             ((long long)(u.token0 + x * p.tq + t) * p.num_q_heads + kh * p.group + g) * D +
+             lane * VPL;
+    if constexpr (VPL == 4)
+      *reinterpret_cast<uint2 *>(dst) = make_uint2(Mma<T>::pack(num[0] * inv, num[1] * inv),
+                                                   Mma<T>::pack(num[2] * inv, num[3] * inv));
+    else
+      *reinterpret_cast<uint32_t *>(dst) = Mma<T>::pack(num[0] * inv, num[1] * inv);
+  }
+}
+
+}  // namespace pa

@@ -1,5 +1,6 @@
 // C entry points around the 8-bit paged cache: rotary positions with the cache
-// write, decode attention, gather and block copies.  Included at the end of
+// write, decode attention, gather and block copies, and attention over packed
+// prompts.  Included at the end of
 // pa_kernels.cu, whose helpers (tensor-map encoder, argument checks, wait
 // limit) it uses.
 #pragma once
@@ -201,6 +202,89 @@ int launch_decode_fp8(pa::DecodeFp8Params &p, const CUtensorMap &kmap, const CUt
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+// ---------------------------------------------------------------- packed prompts
+
+// K or V [Tk, Hkv, D] with any token stride as a 3-D map (D, Hkv, Tk); a box is
+// 64 columns of one head x 128 tokens.  Q [T, Hq, D] the same way, a box 64
+// columns x the G heads of one kv head x tq tokens.
+bool encode_rows_map(CUtensorMap *m, const void *base, long long rows, int heads, int D,
+                     long long stride, int box_heads, int box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+  cuuint32_t box[3] = {64u, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// How a call is cut up: units of (pair of query tiles, kv head), at most
+// `units` of them, and pieces of the keys when the units alone leave SMs idle.
+struct PromptPlan {
+  long long units;
+  int tq, pieces, piece_tiles;
+  size_t workspace;
+};
+
+PromptPlan plan_prompt(int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads,
+                       int head_dim, int max_query, int max_key, int sms) {
+  PromptPlan pl;
+  pl.tq = pa::kPrRows / (num_q_heads / num_kv_heads);
+  const long long w = 2 * pl.tq;
+  const long long pairs = std::min((long long)num_seqs * ((max_query + w - 1) / w),
+                                   num_tokens / w + num_seqs);
+  pl.units = pairs * num_kv_heads;
+  const long long tiles = std::max(1, (max_key + pa::kPrKeys - 1) / pa::kPrKeys);
+  pl.pieces = 1;
+  pl.piece_tiles = (int)tiles;
+  if (pl.units < sms) {
+    const long long per = std::max(4ll, (pl.units * tiles + 2 * sms - 1) / (2 * sms));
+    if (per < tiles) {
+      pl.piece_tiles = (int)per;
+      pl.pieces = (int)((tiles + per - 1) / per);
+    }
+  }
+  pl.workspace = pl.pieces > 1 ? (size_t)pl.units * pl.pieces * 256 * (head_dim * 4 + 8) : 0;
+  return pl;
+}
+
+// What plan_prompt takes; out of range for the entry points below.
+int check_prompt(int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                 int max_query, int max_key) {
+  if (num_seqs < 0 || num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+      max_query < 0 || max_key < 0 || num_q_heads % num_kv_heads != 0)
+    return PA_ERR_ARG;
+  if ((head_dim != 64 && head_dim != 128) || num_q_heads / num_kv_heads > 16 ||
+      num_q_heads > 65536 || max_query >= (1 << 30) || max_key >= (1 << 30) ||
+      num_tokens >= (1 << 30))
+    return PA_ERR_UNSUPPORTED;
+  return PA_OK;
+}
+
+template <typename T, int D>
+int launch_prompt(pa::PromptParams &p, const PromptPlan &pl, const CUtensorMap &qmap,
+                  const CUtensorMap &kmap, const CUtensorMap &vmap, int dev, cudaStream_t stream) {
+  auto kern = pa::prompt_attention_kernel<T, D>;
+  constexpr int smem = pa::PromptSmem<D>::BYTES;
+  static std::atomic<int> attr_set[kMaxDevices];
+  if (!attr_set[dev].load()) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+        cudaSuccess)
+      return PA_ERR_CUDA;
+    attr_set[dev].store(1);
+  }
+  if (launch_dependent(kern, dim3((unsigned)(pl.units * pl.pieces)), pa::kPrThreads, smem, stream,
+                       qmap, kmap, vmap, p) != cudaSuccess)
+    return PA_ERR_CUDA;
+  if (pl.pieces > 1 &&
+      launch_dependent(pa::prompt_join_kernel<T, D>, dim3((unsigned)pl.units, 8), 256, 0, stream,
+                       p) != cudaSuccess)
+    return PA_ERR_CUDA;
+  return PA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -334,7 +418,7 @@ int pa_gather_cache_fp8(void *key, void *value, const void *k_cache, const void 
   if (!supported_shape(head_dim, block_size)) return PA_ERR_UNSUPPORTED;
   if (num_seqs == 0 || num_tokens == 0) return PA_OK;
   if (max_blocks_per_seq <= 0 || num_blocks <= 0) return PA_ERR_ARG;
-  if (num_kv_heads >= (1 << 20) || num_tokens >= (1 << 31) - pa::kGatherRows)
+  if (num_kv_heads >= (1 << 20) || num_tokens >= (1ll << 31) - pa::kGatherRows)
     return PA_ERR_UNSUPPORTED;
   if (!key || !value || !k_cache || !v_cache || !kv_scale || !block_tables || !key_start)
     return PA_ERR_ARG;
@@ -377,6 +461,91 @@ int pa_gather_cache_fp8(void *key, void *value, const void *k_cache, const void 
             ? launch_dependent(pa::gather_cache_fp8_kernel<__half, 128>, grid, 256, 0, st, p)
             : launch_dependent(pa::gather_cache_fp8_kernel<__half, 64>, grid, 256, 0, st, p);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+size_t pa_prompt_attention_workspace_bytes(int num_seqs, int num_tokens, int num_q_heads,
+                                           int num_kv_heads, int head_dim, int max_query_len,
+                                           int max_key_len) {
+  if (check_prompt(num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim, max_query_len,
+                   max_key_len) != PA_OK)
+    return 0;
+  int dev;
+  if (current_device(&dev) != PA_OK) return 0;
+  const int sms = sm_count(dev);
+  if (sms <= 0) return 0;
+  return plan_prompt(num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim, max_query_len,
+                     max_key_len, sms)
+      .workspace;
+}
+
+int pa_prompt_attention(void *out, const void *q, const void *key, const void *value,
+                        const int32_t *query_start, const int32_t *key_start, float scale,
+                        int num_kv_heads, int num_seqs, int num_tokens, int num_key_tokens,
+                        int num_q_heads, int head_dim, int max_query_len, int max_key_len,
+                        int64_t q_stride, int64_t key_stride, int64_t value_stride, pa_dtype dtype,
+                        void *workspace, size_t workspace_bytes, pa_stream_t stream) {
+  if (num_key_tokens < 0 || (dtype != PA_F16 && dtype != PA_BF16)) return PA_ERR_ARG;
+  const int bad = check_prompt(num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim,
+                               max_query_len, max_key_len);
+  if (bad != PA_OK) return bad;
+  if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return PA_OK;
+  if (!out || !q || !query_start || !key_start || (num_key_tokens > 0 && (!key || !value)))
+    return PA_ERR_ARG;
+  if (!aligned(out, 16) || !aligned(q, 16) || !aligned(key, 16) || !aligned(value, 16) ||
+      !aligned(query_start, 4) || !aligned(key_start, 4))
+    return PA_ERR_ARG;
+  if (!aligned_stride(q_stride, head_dim, num_q_heads) ||
+      !aligned_stride(key_stride, head_dim, num_kv_heads) ||
+      !aligned_stride(value_stride, head_dim, num_kv_heads))
+    return PA_ERR_ARG;
+  if (q_stride >= (1ll << 38) || key_stride >= (1ll << 38) || value_stride >= (1ll << 38))
+    return PA_ERR_UNSUPPORTED;
+  int dev;
+  if (current_device(&dev) != PA_OK || dev >= kMaxDevices) return PA_ERR_CUDA;
+  const int sms = sm_count(dev);
+  if (sms <= 0) return PA_ERR_CUDA;
+  const PromptPlan pl = plan_prompt(num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim,
+                                    max_query_len, max_key_len, sms);
+  if (pl.units * pl.pieces >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+  if (pl.workspace > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < pl.workspace))
+    return PA_ERR_WORKSPACE;
+  const int G = num_q_heads / num_kv_heads;
+  // without keys the maps of K and V are never read: they describe q then
+  const bool keys = num_key_tokens > 0;
+  CUtensorMap qmap, kmap, vmap;
+  if (!encode_rows_map(&qmap, q, num_tokens, num_q_heads, head_dim, q_stride, G, pl.tq) ||
+      !encode_rows_map(&kmap, keys ? key : q, keys ? num_key_tokens : num_tokens, num_kv_heads,
+                       head_dim, keys ? key_stride : q_stride, 1, pa::kPrKeys) ||
+      !encode_rows_map(&vmap, keys ? value : q, keys ? num_key_tokens : num_tokens, num_kv_heads,
+                       head_dim, keys ? value_stride : q_stride, 1, pa::kPrKeys))
+    return PA_ERR_CUDA;
+  pa::PromptParams p;
+  p.out = out;
+  p.query_start = query_start;
+  p.key_start = key_start;
+  p.part_o = static_cast<float *>(workspace);
+  p.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) +
+                                         (size_t)pl.units * pl.pieces * 256 * head_dim * 4);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.num_seqs = num_seqs;
+  p.num_tokens = num_tokens;
+  p.num_key_tokens = num_key_tokens;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.group = G;
+  p.tq = pl.tq;
+  p.max_query = max_query_len;
+  p.max_key = max_key_len;
+  p.pieces = pl.pieces;
+  p.piece_tiles = pl.piece_tiles;
+  p.wait_ns = g_wait_limit_ns.load();
+  cudaStream_t st = (cudaStream_t)stream;
+  if (dtype == PA_BF16)
+    return head_dim == 128
+               ? launch_prompt<__nv_bfloat16, 128>(p, pl, qmap, kmap, vmap, dev, st)
+               : launch_prompt<__nv_bfloat16, 64>(p, pl, qmap, kmap, vmap, dev, st);
+  return head_dim == 128 ? launch_prompt<__half, 128>(p, pl, qmap, kmap, vmap, dev, st)
+                         : launch_prompt<__half, 64>(p, pl, qmap, kmap, vmap, dev, st);
 }
 
 }  // extern "C"
