@@ -8,30 +8,41 @@
 //
 // Work split, launch plan and split merge are those of the 16-bit decode
 // kernel (decode_attention.cuh): the tiles of all (sequence, kv head) pairs,
-// numbered in order, are cut into equal contiguous ranges, one per warp, each
-// warp streams its range through its own ring of bulk copies, and cut
-// segments leave partials for the merge kernel.  Here a tile is 32 tokens
+// numbered in order, are cut into equal contiguous ranges, one per warp, and
+// cut segments leave partials for the merge kernel.  Here a tile is 32 tokens
 // whatever the block size (two blocks of 16 or one of 32): half the bytes per
 // token would otherwise leave twice the bookkeeping per byte.
 //
-// Arithmetic.  Codes become fp16 exactly (cvt.rn.f16x2.e4m3x2), so both
-// products are fp16 warp MMAs (m16n8k16, fp32 accumulation) for fp16 and bf16
-// queries alike:
-//   * a query row is scaled by the power of two that puts its largest element
+// A warp has one buffer for K and one for V, filled by 16-byte asynchronous
+// copies: the next tile's K is asked for as soon as the scores are made, its V
+// after P.V, so either is on its way during about half of a tile's work, and 8
+// to 16 warps per SM cover for each other.  (Bulk tensor copies, six of them a
+// tile, took 1400 of a warp's 5900 cycles per tile to issue.)
+//
+// Arithmetic.
+//   * Codes become fp16 exactly (cvt.rn.f16x2.e4m3x2) and both products are
+//     fp16 warp MMAs (m16n8k16, fp32 accumulation) for fp16 and bf16 queries
+//     alike.  (The e4m3 warp MMA on e4m3 pieces of the queries was built too:
+//     the decode of 256 mixed sequences took 103 us with it, 97 with this.)
+//   * A query row is scaled by the power of two that puts its largest element
 //     in [2^14, 2^15) before it is rounded to fp16: exact for fp16 queries and
-//     for bf16 elements down to 2^-39 of the row's largest;
-//   * a weight times its vs_t is scaled by the power of two that puts the
+//     for bf16 elements down to 2^-39 of the row's largest.
+//   * A weight times its vs_t is scaled by the power of two that puts the
 //     tile's largest vs in the same range and goes in as a hi + lo pair of
-//     fp16 values (2^-22 relative), so the output keeps ~fp32 accuracy;
-//   * a tile's P.V is summed in fresh accumulators and folded into the running
+//     fp16 values (2^-22 relative), so the output keeps ~fp32 accuracy.
+//   * Groups of up to four heads (HPL = 1) give each head two neighbouring of
+//     the eight MMA columns: a lane then holds the scores of one head, half the
+//     softmax work, and hi and lo share one P.V MMA.  Wider groups (HPL = 2)
+//     need the columns for heads and take two.
+//   * A tile's P.V is summed in fresh accumulators and folded into the running
 //     output by one FMA with the softmax correction, so long segments never
 //     add small products to a large tensor-core accumulator.
 // Fragments come from shared memory by plain 16-byte loads, not ldmatrix: the
 // reduction order of an MMA is free as long as both operands agree, so lane
 // (g, c) takes D/4 neighbouring codes of K row g, and D/8 neighbouring columns
 // of V for its four tokens; bytes of two tokens are paired with one byte
-// permute before the conversion.  With the copies' 128-byte (D = 128) or
-// 64-byte (D = 64) swizzle the K loads and D = 128's V loads are free of bank
+// permute before the conversion.  Chunks are swizzled within 128-byte (D = 128)
+// or 64-byte (D = 64) rows, with which the K loads and D = 128's V loads are free of bank
 // conflicts.
 //
 // Bound: HBM, 2 D + 8 bytes per token and kv head.
@@ -47,6 +58,7 @@ constexpr int kF8Tile = 32;   // tokens per tile
 
 struct DecodeFp8Params {
   DecodeParams d;             // max_blocks counts tiles of 32 tokens here
+  const uint8_t *k_cache, *v_cache;
   const float *kv_scale;
   int table_blocks;           // blocks per row of the block table
   int block_size;
@@ -78,22 +90,16 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
-  return v;
+// 16 bytes global -> shared, asynchronously, and the groups they complete in.
+__device__ __forceinline__ void copy16_async(void *dst, const void *src, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)),
+               "l"(reinterpret_cast<uint64_t>(src)), "l"(policy)
+               : "memory");
 }
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ float lds_f32(uint32_t a) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
-  return v;
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {   // all but this thread's last N groups have landed
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ void st_global_hint4(float *dst, float4 v, uint64_t policy) {
@@ -113,38 +119,63 @@ __device__ __forceinline__ int scale_field(uint32_t bits) {
   return min(max(e, 15), 254);
 }
 
-template <int D, int NT>
+// D = A B (+ C), A and B fp16.
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1, const float *c) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
+        "f"(c[2]), "f"(c[3]));
+}
+
+// NT sets of 4 HPL heads; lane (g, c) works on heads (4 n + c) HPL + e of set n.
+template <int D, int NT, int HPL>
 struct Fp8Path {
-  static constexpr int W = D / 16;    // words of K per lane and row = k-steps of q.K
-  static constexpr int MM = D / 16;   // m-tiles of P.V
-  float o[MM][NT][4];                 // d = (D/8) g + 2 mm + (r >> 1), head 8 n + 2 c + (r & 1)
-  float m[NT][2], l[NT][2];
-  float qs[NT][2];                    // scale * log2(e) * 2^-shift of the accumulators' heads
+  static constexpr int W = D / 16;           // words of K per lane and row = k-steps of q.K
+  static constexpr int MM = D / 16;          // m-tiles of P.V
+  float o[MM][NT][HPL][2];                   // d = (D/8) g + 2 mm + r
+  float m[NT][HPL], l[NT][HPL];
+  float qs[NT][HPL];                         // scale * log2(e) * 2^-shift of the head's q
   uint32_t qf[W][NT][2];
+  int k_off[2], v_off[2];                    // this lane's chunks of K rows g, V rows 2 c and 2 c + 1
+
+  __device__ __forceinline__ void init(int lane) {
+    const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = 2 * c + i;
+      if constexpr (D == 128) {
+        k_off[i] = g * 128 + (((2 * c + i) ^ g) << 4);
+        v_off[i] = row * 128 + ((g ^ row) << 4);
+      } else {
+        k_off[i] = g * 64 + ((c ^ (g >> 1)) << 4);   // one chunk a row: i = 1 is not used
+        v_off[i] = row * 64 + (((g >> 1) ^ (row >> 1)) << 4) + (g & 1) * 8;
+      }
+    }
+    reset();
+  }
 
   __device__ __forceinline__ void reset() {
 #pragma unroll
-    for (int a = 0; a < MM; ++a)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) o[a][n][r] = 0.f;
-#pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        m[n][r] = -INFINITY;
-        l[n][r] = 0.f;
+      for (int e = 0; e < HPL; ++e) {
+#pragma unroll
+        for (int a = 0; a < MM; ++a) o[a][n][e][0] = o[a][n][e][1] = 0.f;
+        m[n][e] = -INFINITY;
+        l[n][e] = 0.f;
       }
   }
 
-  // Lane (g, c): columns (D/4) c .. of query row 8 n + g, as scaled fp16.
+  // Lane (g, c): columns (D/4) c .. of the query row of MMA column g, as scaled fp16.
   __device__ __forceinline__ void load_q(const uint8_t *q, int G, bool bf16, float scale_log2,
                                          int lane) {
     const int g = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int head = n * 8 + g;
+      const int head = HPL == 1 ? n * 4 + (g >> 1) : n * 8 + g;
       uint32_t raw[2 * W];
       uint32_t top = 0;
       const uint4 *row = reinterpret_cast<const uint4 *>(q + (size_t)head * (D * 2) + c * (D / 2));
@@ -168,111 +199,117 @@ struct Fp8Path {
         const float2 f = bf16 ? Mma<__nv_bfloat16>::unpack(raw[i]) : Mma<__half>::unpack(raw[i]);
         qf[i >> 1][n][i & 1] = Mma<__half>::pack(f.x * up, f.y * up);
       }
-      qs[n][0] = __shfl_sync(0xffffffffu, down, 8 * c);        // row 2 c is held by lanes 8 c ..
-      qs[n][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
+#pragma unroll
+      for (int e2 = 0; e2 < HPL; ++e2)       // column 2 c + e2 was loaded by lanes 8 c + 4 e2 ..
+        qs[n][e2] = __shfl_sync(0xffffffffu, down, 8 * c + 4 * e2);
     }
   }
 
-  // One tile: codes at kb, vb, scales at sb ([block][K or V][B] floats), `live`
-  // the tokens that count.
-  __device__ __forceinline__ void tile(uint32_t kb, uint32_t vb, uint32_t sb, int B, uint32_t live,
-                                       int lane) {
-    const int g = lane >> 2, c = lane & 3;
-    float sc[2][NT][4];
-    // ---- scores: S^T[token][head]
+  float sc[2][NT][2][HPL];     // scores of tokens 16 t + g + 8 x
+
+  // Scores of one tile, S^T[token][head]: K codes at kb, their scales at ksc.
+  __device__ __forceinline__ void scores(const uint8_t *kb, const float *ksc, int lane) {
+    const int g = lane >> 2;
+    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) sc[t][n][r] = 0.f;
-      uint32_t k0[W], k1[W];   // rows 16 t + g and + 8
+      uint32_t k0[W], k1[W];     // rows 16 t + g and + 8 (the same swizzle)
 #pragma unroll
       for (int i = 0; i < W / 4; ++i) {
-        const int row = 16 * t + g;
-        uint32_t a;
-        if constexpr (D == 128)
-          a = kb + row * 128 + (((2 * c + i) ^ g) << 4);
-        else
-          a = kb + row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
-        const uint4 v = lds128(a), u = lds128(a + 8 * D);   // row + 8: the same swizzle
+        const uint8_t *a = kb + k_off[i] + t * (16 * D);
+        const uint4 v = *reinterpret_cast<const uint4 *>(a);
+        const uint4 u = *reinterpret_cast<const uint4 *>(a + 8 * D);
         k0[4 * i] = v.x, k0[4 * i + 1] = v.y, k0[4 * i + 2] = v.z, k0[4 * i + 3] = v.w;
         k1[4 * i] = u.x, k1[4 * i + 1] = u.y, k1[4 * i + 2] = u.z, k1[4 * i + 3] = u.w;
       }
+      float s[NT][4];
 #pragma unroll
       for (int w = 0; w < W; ++w) {
         const uint32_t a[4] = {e4m3x2_to_f16x2(k0[w]), e4m3x2_to_f16x2(k1[w]),
                                e4m3x2_hi_to_f16x2(k0[w]), e4m3x2_hi_to_f16x2(k1[w])};
 #pragma unroll
-        for (int n = 0; n < NT; ++n) Mma<__half>::run(sc[t][n], a, qf[w][n][0], qf[w][n][1]);
+        for (int n = 0; n < NT; ++n) mma_f16(s[n], a, qf[w][n][0], qf[w][n][1], w == 0 ? zero : s[n]);
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float ks = ksc[16 * t + g + 8 * x];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < HPL; ++e) sc[t][n][x][e] = s[n][2 * x + e] * (ks * qs[n][e]);
       }
     }
-    // ---- the tokens' scales: K's for the scores, V's for the weights
+  }
+
+  // The same tile's part of the output: V codes at vb, their scales at vsc,
+  // `live` the tokens that count.
+  __device__ __forceinline__ void output(const uint8_t *vb, const float *vsc, uint32_t live,
+                                         int lane) {
+    const int g = lane >> 2, c = lane & 3;
+    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
     float vs[2][2];
-    {
-      const int sub = lane / B;
-      const uint32_t mine = sb + 4 * ((2 * sub + 1) * B + lane - sub * B);   // V scale of token `lane`
-      const uint32_t bits =
-          (live >> lane) & 1 ? __float_as_uint(fabsf(lds_f32(mine))) : 0u;
-      const int e = scale_field(__reduce_max_sync(0xffffffffu, bits));
-      const float up = pow2_field(268 - e);
-      vdown = pow2_field(e - 14);
+    const uint32_t bits = (live >> lane) & 1 ? __float_as_uint(fabsf(vsc[lane])) : 0u;
+    const int top = scale_field(__reduce_max_sync(0xffffffffu, bits));
+    const float up = pow2_field(268 - top);
+    const float vdown = pow2_field(top - 14);   // 2^-shift of the weights
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) vs[t][x] = vsc[16 * t + g + 8 * x] * up;
+    if (live != 0xffffffffu) {                  // tokens that do not count
+      const uint32_t mask = live >> g;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int tok = 16 * t + g + 8 * x, s = tok / B;
-          const uint32_t a = sb + 4 * (2 * s * B + tok - s * B);
-          const bool on = (live >> tok) & 1;
-          const float ks = lds_f32(a);
-          vs[t][x] = on ? lds_f32(a + 4 * B) * up : 0.f;
+        for (int x = 0; x < 2; ++x)
+          if (!((mask >> (16 * t + 8 * x)) & 1)) {
+            vs[t][x] = 0.f;
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
-              sc[t][n][2 * x + r] = on ? sc[t][n][2 * x + r] * (ks * qs[n][r]) : -INFINITY;
-        }
+              for (int e = 0; e < HPL; ++e) sc[t][n][x][e] = -INFINITY;
+          }
     }
-    // ---- running maximum and sum of each head
-    float alpha[NT][2];
+    // ---- running maximum and sum of each head; weights (times vs) as B operands
+    float alpha[NT][HPL];
+    uint32_t ph[2][NT][2], pl[2][NT][2];     // HPL = 1: hi and lo both in ph
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+      float hi[HPL][2][2], lo[HPL][2][2];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        float v = fmaxf(fmaxf(sc[0][n][r], sc[0][n][2 + r]), fmaxf(sc[1][n][r], sc[1][n][2 + r]));
+      for (int e = 0; e < HPL; ++e) {
+        float v = fmaxf(fmaxf(sc[0][n][0][e], sc[0][n][1][e]), fmaxf(sc[1][n][0][e], sc[1][n][1][e]));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-        const float mn = fmaxf(m[n][r], v);
+        const float mn = fmaxf(m[n][e], v);
         // all scores so far -inf (a -inf in q or K): weights of 0, not NaN
         const float ref = mn == -INFINITY ? 0.f : mn;
-        alpha[n][r] = exp2_approx(m[n][r] - ref);
-        m[n][r] = mn;
-        float s = 0.f;
+        alpha[n][e] = exp2_approx(m[n][e] - ref);
+        m[n][e] = mn;
+        float sum = 0.f;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const float pv = exp2_approx(sc[t][n][2 * x + r] - ref);
-            sc[t][n][2 * x + r] = pv * vs[t][x];
-            s += pv;
+            const float pv = exp2_approx(sc[t][n][x][e] - ref);
+            sum += pv;
+            const float y = pv * vs[t][x];
+            hi[e][t][x] = __half2float(__float2half_rn(y));
+            lo[e][t][x] = y - hi[e][t][x];
           }
-        l[n][r] = l[n][r] * alpha[n][r] + s;
+        l[n][e] = l[n][e] * alpha[n][e] + sum;
       }
-    // ---- weights (times vs) as B operands: hi + lo
-    uint32_t ph[2][NT][2], pl[2][NT][2];
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const float a = sc[t][n][2 * x], b = sc[t][n][2 * x + 1];
-          const uint32_t h = Mma<__half>::pack(a, b);
-          const float2 f = Mma<__half>::unpack(h);
-          ph[t][n][x] = movmatrix_trans(h);
-          pl[t][n][x] = movmatrix_trans(Mma<__half>::pack(a - f.x, b - f.y));
+          ph[t][n][x] = movmatrix_trans(
+              Mma<__half>::pack(hi[0][t][x], HPL == 1 ? lo[0][t][x] : hi[HPL - 1][t][x]));
+          if constexpr (HPL == 2)
+            pl[t][n][x] = movmatrix_trans(Mma<__half>::pack(lo[0][t][x], lo[1][t][x]));
         }
+    }
     // ---- O^T[d][head] = alpha O^T + 2^.. V^T P^T
     constexpr int XW = D / 32;   // words of V per lane and token
     uint32_t vw[2][4][XW];       // tokens 16 t + 2 c + {0, 1, 8, 9}
@@ -280,19 +317,25 @@ struct Fp8Path {
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int row = 16 * t + 2 * c + (i & 1) + 8 * (i >> 1);
+        const uint8_t *a = vb + v_off[i & 1] + (16 * t + 8 * (i >> 1)) * D;
         if constexpr (D == 128) {
-          const uint4 v = lds128(vb + row * 128 + ((g ^ (row & 7)) << 4));
+          const uint4 v = *reinterpret_cast<const uint4 *>(a);
           vw[t][i][0] = v.x, vw[t][i][1] = v.y, vw[t][i][2] = v.z, vw[t][i][3] = v.w;
         } else {
-          const uint2 v = lds64(vb + row * 64 + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
+          const uint2 v = *reinterpret_cast<const uint2 *>(a);
           vw[t][i][0] = v.x, vw[t][i][1] = v.y;
         }
-        // a token that does not count may hold any bits, NaN codes too
-        if (live != 0xffffffffu && !((live >> row) & 1))
-#pragma unroll
-          for (int x = 0; x < XW; ++x) vw[t][i][x] = 0u;
       }
+    if (live != 0xffffffffu) {   // a token that does not count may hold any bits, NaN codes too
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = 16 * t + 2 * c + (i & 1) + 8 * (i >> 1);
+#pragma unroll
+          for (int x = 0; x < XW; ++x) vw[t][i][x] = (live >> row) & 1 ? vw[t][i][x] : 0u;
+        }
+    }
 #pragma unroll
     for (int x = 0; x < XW; ++x)
 #pragma unroll
@@ -301,10 +344,6 @@ struct Fp8Path {
         const uint32_t sel = y ? 0x7362u : 0x5140u;   // bytes 2 y, 2 y + 1 of both tokens
         float acc[NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[n][r] = 0.f;
-#pragma unroll
         for (int t = 0; t < 2; ++t) {
           const uint32_t u = __byte_perm(vw[t][0][x], vw[t][1][x], sel);
           const uint32_t v = __byte_perm(vw[t][2][x], vw[t][3][x], sel);
@@ -312,18 +351,21 @@ struct Fp8Path {
                                  e4m3x2_hi_to_f16x2(v)};
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            Mma<__half>::run(acc[n], f, ph[t][n][0], ph[t][n][1]);
-            Mma<__half>::run(acc[n], f, pl[t][n][0], pl[t][n][1]);
+            mma_f16(acc[n], f, ph[t][n][0], ph[t][n][1], t == 0 ? zero : acc[n]);
+            if constexpr (HPL == 2) mma_f16(acc[n], f, pl[t][n][0], pl[t][n][1], acc[n]);
           }
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            o[a][n][r] = fmaf(acc[n][r], vdown, o[a][n][r] * alpha[n][r & 1]);
+          for (int e = 0; e < HPL; ++e)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float add = HPL == 1 ? acc[n][2 * r] + acc[n][2 * r + 1] : acc[n][2 * r + e];
+              o[a][n][e][r] = fmaf(add, vdown, o[a][n][e][r] * alpha[n][e]);
+            }
       }
   }
-  float vdown;   // 2^-shift of the current tile's weights
 
   // Write the segment: normalised output, or a partial for the merge.
   __device__ __forceinline__ void finish(const DecodeParams &p, int s, int h, bool complete,
@@ -334,12 +376,12 @@ struct Fp8Path {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        float lt = l[n][r];
+      for (int e = 0; e < HPL; ++e) {
+        float lt = l[n][e];
         lt += __shfl_xor_sync(0xffffffffu, lt, 4);
         lt += __shfl_xor_sync(0xffffffffu, lt, 8);
         lt += __shfl_xor_sync(0xffffffffu, lt, 16);
-        const int head = n * 8 + 2 * c + r;
+        const int head = (n * 4 + c) * HPL + e;
         if (head >= G) continue;
         const float f = complete ? (lt == 0.f ? 0.f : 1.f / lt) : 1.f;
         float *dst = (complete ? p.out + ((int64_t)s * p.num_q_heads + (int64_t)h * G) * D
@@ -347,8 +389,8 @@ struct Fp8Path {
                      head * D + (D / 8) * g;
 #pragma unroll
         for (int a = 0; a < MM; a += 2) {
-          const float4 v = make_float4(o[a][n][r] * f, o[a][n][2 + r] * f, o[a + 1][n][r] * f,
-                                       o[a + 1][n][2 + r] * f);
+          const float4 v = make_float4(o[a][n][e][0] * f, o[a][n][e][1] * f, o[a + 1][n][e][0] * f,
+                                       o[a + 1][n][e][1] * f);
           if (complete)
             *reinterpret_cast<float4 *>(dst + 2 * a) = v;
           else
@@ -356,88 +398,124 @@ struct Fp8Path {
         }
         if (!complete && g == 0) {
           float *pm = p.part_ml + ((int64_t)slot * G + head) * 2;
-          st_global_hint(pm, m[n][r], pol);
+          st_global_hint(pm, m[n][e], pol);
           st_global_hint(pm + 1, lt, pol);
         }
       }
   }
 };
 
-// Lane-parallel description of up to 32 consecutive tiles of one sequence.
-struct Fp8Batch {
-  int s, L, nt;             // warp-uniform: sequence, its length, its tiles
-  int n;                    // tiles in the batch (0 = none)
-  int my_h, my_j;           // this lane's tile
-  int id0, id1;             // its blocks (block size 32: id1 unused)
+// A tile as its warp's ring holds it: rows of its tokens 0 and 16 in the code
+// pools (-1: no such block), the tokens that count, TF_ flags and kv head << 8.
+struct Fp8Tile {
+  int row0, row1;
+  uint32_t live;
+  int head_flags;
+};
+constexpr int kF8Ring = 64;
+
+// The walk of a warp through its tiles, described up to 32 at a time, lane by
+// lane: begin() fetches the block ids of the next run of tiles of one
+// sequence, end() writes the run into the ring.
+struct Fp8Walk {
+  int s, L, nt, h, j;        // next tile to describe (warp-uniform)
+  int described;             // tiles described so far
+  int n;                     // tiles between begin() and end()
+  int id0, id1, my_h, my_j;  // this lane's tile of them
+
+  __device__ __forceinline__ void begin(const DecodeFp8Params &p, int ntiles, int lane) {
+    while (h >= p.d.num_kv_heads || nt == 0) {   // next sequence with tiles
+      h = 0;
+      j = 0;
+      if (s + 1 >= p.d.num_seqs) {   // only if lengths changed under the kernel: empty tiles
+        L = 0;
+        nt = 1;
+        break;
+      }
+      ++s;
+      L = seq_len_clamped<kF8Tile>(p.d, s);
+      nt = ceil_div_i(L, kF8Tile);
+    }
+    const int64_t left = (int64_t)(p.d.num_kv_heads - h) * nt - j;
+    n = min((int)min(left, (int64_t)32), ntiles - described);
+    my_h = h;
+    my_j = j + lane;                 // a few steps, one when nt >= 32
+    while (my_j >= nt) my_j -= nt, ++my_h;
+    id0 = id1 = -1;
+    if (lane < n) {
+      const int per = kF8Tile / p.block_size, b0 = my_j * per;
+      const int32_t *table = p.d.block_tables + (int64_t)s * p.table_blocks + b0;
+      const bool two = per == 2 && L - my_j * kF8Tile > p.block_size;
+      if (b0 < p.table_blocks) id0 = __ldg(table);
+      if (two && b0 + 1 < p.table_blocks) id1 = __ldg(table + 1);
+    }
+  }
+
+  __device__ __forceinline__ void end(const DecodeFp8Params &p, Fp8Tile *ring, int *ring_s,
+                                      int ntiles, int lane) {
+    if (lane < n) {
+      const int B = p.block_size, per = kF8Tile / B;
+      const int len = min(kF8Tile, L - my_j * kF8Tile);
+      const uint32_t below = len == 32 ? 0xffffffffu : (1u << len) - 1u;
+      const bool in0 = id0 >= 0 && id0 < p.d.num_blocks, in1 = id1 >= 0 && id1 < p.d.num_blocks;
+      const bool first = my_j == 0, last = my_j == nt - 1;
+      const int at = described + lane;
+      Fp8Tile t;
+      t.row0 = in0 ? (id0 * p.d.num_kv_heads + my_h) * B : -1;
+      t.row1 = per == 1 ? (in0 ? t.row0 + 16 : -1)
+                        : (in1 ? (id1 * p.d.num_kv_heads + my_h) * B : -1);
+      t.live = below & ((in0 ? (per == 2 ? 0x0000ffffu : 0xffffffffu) : 0u) |
+                        (in1 ? 0xffff0000u : 0u));
+      t.head_flags = (my_h << 8) | (first || at == 0 ? TF_FIRST : 0) | (first ? TF_J0 : 0) |
+                     (last || at == ntiles - 1 ? TF_LAST : 0) | (last ? TF_JEND : 0);
+      if (t.live != below)           // a block outside the pool, or past the table's end
+        flag_error(my_j * per + (in0 ? 1 : 0) >= p.table_blocks ? PA_DEVERR_CONTEXT_LEN
+                                                                : PA_DEVERR_BLOCK_ID);
+      ring[at & (kF8Ring - 1)] = t;
+      ring_s[at & (kF8Ring - 1)] = s;
+    }
+    const int last_h = __shfl_sync(0xffffffffu, my_h, n - 1);
+    const int last_j = __shfl_sync(0xffffffffu, my_j, n - 1);
+    described += n;
+    n = 0;
+    h = last_h + (last_j == nt - 1 ? 1 : 0);
+    j = last_j == nt - 1 ? 0 : last_j + 1;
+    __syncwarp();
+  }
 };
 
-__device__ __forceinline__ void make_fp8_batch(const DecodeFp8Params &p, Fp8Batch &tb, int s, int L,
-                                               int nt, int h, int j, int64_t remaining, int lane) {
-  tb.s = s;
-  tb.L = L;
-  tb.nt = nt;
-  const int64_t left = (int64_t)p.d.num_kv_heads * nt - ((int64_t)h * nt + j);
-  const int64_t n = left < remaining ? left : remaining;
-  tb.n = n < 32 ? (int)n : 32;
-  tb.my_h = 0;
-  tb.my_j = 0;
-  tb.id0 = tb.id1 = -1;
-  if (lane < tb.n) {
-    const int64_t at = (int64_t)h * nt + j + lane;
-    tb.my_h = (int)(at / nt);
-    tb.my_j = (int)(at - (int64_t)tb.my_h * nt);
-    const int32_t *row = p.d.block_tables + (int64_t)s * p.table_blocks;
-    const int per = kF8Tile / p.block_size, b0 = tb.my_j * per;
-    const int used = min(ceil_div_i(L, p.block_size), p.table_blocks);
-    if (b0 < used) tb.id0 = __ldg(row + b0);
-    if (per == 2 && b0 + 1 < used) tb.id1 = __ldg(row + b0 + 1);
-  }
+// Smem of one warp: a K and a V tile, their scales, the group's query rows, a
+// ring of tile descriptions.
+__host__ __device__ constexpr int fp8_warp_bytes(int D, int G) {
+  return 2 * kF8Tile * D + 2 * kF8Tile * 4 + G * D * 2 + kF8Ring * (int)(sizeof(Fp8Tile) + 4);
 }
 
-// Smem of one CTA: per warp and stage a K and a V tile, 64 scales, the group's
-// query rows, a tile descriptor and a barrier.
-__host__ __device__ constexpr int fp8_stage_bytes(int D) { return 2 * kF8Tile * D; }
-constexpr int kF8ScaleBytes = kF8Tile * 2 * 4;
-struct Fp8Tile {
-  int s, h, flags;
-  uint32_t live;
-};
+// CTAs per SM that registers allow.
+__host__ __device__ constexpr int fp8_ctas(int NT, int HPL) {
+  return NT * HPL == 1 ? 4 : (NT * HPL == 2 ? 3 : 2);
+}
 
-template <int D, int NT, int NW>
-__global__ void __launch_bounds__(NW * 32, NT == 1 ? 3 : 2)
-    paged_decode_fp8_kernel(const __grid_constant__ CUtensorMap kmap,
-                            const __grid_constant__ CUtensorMap vmap, const DecodeFp8Params pp) {
+template <int D, int NT, int HPL, int NW>
+__global__ void __launch_bounds__(NW * 32, fp8_ctas(NT, HPL))
+    paged_decode_fp8_kernel(const DecodeFp8Params pp) {
   constexpr int TILE = kF8Tile * D;
-  constexpr int STAGE = fp8_stage_bytes(D);
   const DecodeParams &p = pp.d;
   const int G = p.group, B = pp.block_size;
   const int qbytes = G * D * 2;
-  const int nstage = p.nstage;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int S = p.num_seqs, Hkv = p.num_kv_heads;
 
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int k0 = warp * nstage, all = NW * nstage;
-  uint8_t *stages = smem + (size_t)k0 * STAGE;
-  uint8_t *scales = smem + (size_t)all * STAGE + (size_t)k0 * kF8ScaleBytes;
-  uint8_t *qslots = smem + (size_t)all * (STAGE + kF8ScaleBytes) + (size_t)k0 * qbytes;
-  uint8_t *after_q = smem + (size_t)all * (STAGE + kF8ScaleBytes + qbytes);
-  Fp8Tile *info = reinterpret_cast<Fp8Tile *>(after_q) + k0;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(after_q + (size_t)all * sizeof(Fp8Tile)) + k0;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  uint8_t *kbuf = smem_raw + (size_t)warp * fp8_warp_bytes(D, G), *vbuf = kbuf + TILE;
+  float *ksc = reinterpret_cast<float *>(vbuf + TILE), *vsc = ksc + kF8Tile;
+  uint8_t *qbuf = reinterpret_cast<uint8_t *>(vsc + kF8Tile);
+  Fp8Tile *ring = reinterpret_cast<Fp8Tile *>(qbuf + qbytes);
+  int *ring_s = reinterpret_cast<int *>(ring + kF8Ring);
 
   __shared__ long long red[NW];
   __shared__ int loc_s[NW];
   __shared__ long long loc_base[NW];
   __shared__ int loc_L[NW];
 
-  if (threadIdx.x == 0) {
-    prefetch_tensormap(&kmap);
-    prefetch_tensormap(&vmap);
-  }
-  if (lane == 0)
-    for (int k = 0; k < nstage; ++k) mbar_init(&bars[k], 1);
   grid_dependency_wait();
   allow_dependent_launch();
 
@@ -451,8 +529,6 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 ? 3 : 2)
         return wk < wa_ ? (wk * U_) / wa_ : -1;
       },
       true, red, loc_s, loc_base, loc_L, U, w_active);
-  if (lane == 0) fence_barrier_init();
-  __syncwarp();
   const bool active = w < w_active;
   const long long u0 = active ? (w * U) / w_active : 0;
   const long long u1 = active ? ((w + 1) * U) / w_active : 0;
@@ -485,134 +561,108 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 ? 3 : 2)
     }
     meta[lane] = v;
   }
-  const long long ntiles = u1 - u0;
+  const int ntiles = (int)(u1 - u0);
 
-  // ---- issue cursor
-  Fp8Batch cur, nxt;
-  long long issued = 0;
-  int cur_k = 0;
-  make_fp8_batch(pp, cur, s0, L0, nt0, h0, j0, ntiles, lane);
-  auto follow = [&](const Fp8Batch &b, long long remaining) {   // the batch after b
-    Fp8Batch r = b;
-    r.n = 0;
-    if (remaining <= 0) return r;
-    int h = __shfl_sync(0xffffffffu, b.my_h, b.n - 1);
-    int j = __shfl_sync(0xffffffffu, b.my_j, b.n - 1) + 1;
-    int s = b.s, L = b.L, nt = b.nt;
-    if (j == nt) { j = 0; ++h; }
-    while (h >= Hkv || nt == 0) {   // next sequence with tiles
-      ++s;
-      if (s >= S) return r;
-      L = seq_len_clamped<kF8Tile>(p, s);
-      nt = ceil_div_i(L, kF8Tile);
-      h = 0;
-      j = 0;
-    }
-    make_fp8_batch(pp, r, s, L, nt, h, j, remaining, lane);
-    return r;
+  // ---- the walk, and the copies of a tile
+  Fp8Walk walk;
+  walk.s = s0, walk.L = L0, walk.nt = nt0, walk.h = h0, walk.j = j0;
+  walk.described = 0;
+  walk.begin(pp, ntiles, lane);
+  walk.end(pp, ring, ring_s, ntiles, lane);
+  // the next run, if the ring has room for it: its block ids travel meanwhile
+  auto look_ahead = [&](int consumed) {
+    if (walk.n == 0 && walk.described < ntiles && walk.described - consumed <= kF8Ring - 32)
+      walk.begin(pp, ntiles, lane);
   };
-  nxt = follow(cur, ntiles - cur.n);
+  look_ahead(0);
 
   const uint64_t stream_policy = l2_policy_evict_first();
-  const int per = kF8Tile / B;
-  auto issue = [&](int stage) {
-    if (cur_k == cur.n) {
-      cur = nxt;
-      cur_k = 0;
-      nxt = follow(cur, ntiles - issued - cur.n);
-    }
-    const int h = __shfl_sync(0xffffffffu, cur.my_h, cur_k);
-    const int j = __shfl_sync(0xffffffffu, cur.my_j, cur_k);
-    const int id0 = __shfl_sync(0xffffffffu, cur.id0, cur_k);
-    const int id1 = __shfl_sync(0xffffffffu, cur.id1, cur_k);
-    const int len = min(kF8Tile, cur.L - j * kF8Tile);
-    const bool in0 = id0 >= 0 && id0 < p.num_blocks;
-    const bool in1 = per == 2 && len > B && id1 >= 0 && id1 < p.num_blocks;
-    const bool first = j == 0 || issued == 0;
-    uint64_t *bar = &bars[stage];
-    fence_proxy_async_smem();   // this lane's reads of the stage, before copies into it
-    if (lane == 0) {
-      Fp8Tile ti;
-      ti.s = cur.s;
-      ti.h = h;
-      ti.flags = (first ? TF_FIRST : 0) |
-                 (j == cur.nt - 1 || issued == ntiles - 1 ? TF_LAST : 0) |
-                 (j == 0 ? TF_J0 : 0) | (j == cur.nt - 1 ? TF_JEND : 0);
-      const uint32_t below = len == 32 ? 0xffffffffu : (1u << len) - 1u;
-      ti.live = below & ((in0 ? (per == 2 ? 0x0000ffffu : 0xffffffffu) : 0u) |
-                         (in1 ? 0xffff0000u : 0u));
-      if (ti.live != below) {   // a block outside the pool, or past the table's end
-        const bool past = j * per + (in0 ? 1 : 0) >= pp.table_blocks;
-        flag_error(past ? PA_DEVERR_CONTEXT_LEN : PA_DEVERR_BLOCK_ID);
+  // chunk 32 i + lane of a tile: D / 16 a row, swizzled within the row
+  constexpr int CPR = D / 16, COPIES = kF8Tile * D / 512;
+  const int crow = lane / CPR, cch = lane % CPR;
+  const int dst0 = crow * D + ((D == 128 ? cch ^ crow : cch ^ ((crow >> 1) & 3)) << 4);
+  // K (which = 0) or V of tile i, and their scales
+  auto copy_tile = [&](int which, const Fp8Tile &t) {
+    const uint8_t *pool = (which ? pp.v_cache : pp.k_cache) + lane * 16;
+    uint8_t *dst = which ? vbuf : kbuf;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int row = half ? t.row1 : t.row0;
+      if (row < 0) continue;
+      const uint8_t *src = pool + (int64_t)row * D;
+#pragma unroll
+      for (int i = 0; i < COPIES / 2; ++i) {
+        // (i's part of the row number is a multiple of 4 for D = 128, of 8 for 64)
+        const int at = (half * COPIES / 2 + i) * 512;
+        copy16_async(dst + at + (D == 128 ? dst0 ^ ((i & 1) << 6) : dst0), src + i * 512,
+                     stream_policy);
       }
-      info[stage] = ti;
-      const uint32_t bytes =
-          (in0 + in1) * (2 * B * D + 8 * B) + (first ? (uint32_t)qbytes : 0u);
-      if (bytes)
-        mbar_arrive_expect_tx(bar, bytes);
-      else
-        mbar_arrive(bar);
-      if (first)
-        bulk_load(qslots + (size_t)stage * qbytes,
-                  p.q + ((int64_t)cur.s * p.num_q_heads + (int64_t)h * G) * (D * 2), qbytes, bar);
+      if ((lane >> 2) == half) {
+        const int64_t first =
+            B == 16 ? (int64_t)row * 2 + which * 16 : (int64_t)t.row0 * 2 + which * 32 + half * 16;
+        copy16_async((which ? vsc : ksc) + 4 * lane, pp.kv_scale + first + 4 * (lane & 3),
+                     stream_policy);
+      }
     }
-    __syncwarp();
-    // lanes 0 .. 3 per - 1: K codes, V codes and scales of one block each
-    const int b = lane / 3, kind = lane - 3 * b;
-    if (b < per && (b == 0 ? in0 : in1)) {
-      const int tile = (b == 0 ? id0 : id1) * Hkv + h;
-      uint8_t *dst = stages + (size_t)stage * STAGE + b * B * D;
-      if (kind == 0)
-        tma_load_2d_hint(dst, &kmap, 0, tile * B, bar, stream_policy);
-      else if (kind == 1)
-        tma_load_2d_hint(dst + TILE, &vmap, 0, tile * B, bar, stream_policy);
-      else
-        bulk_load(scales + (size_t)stage * kF8ScaleBytes + b * 8 * B,
-                  pp.kv_scale + (int64_t)tile * 2 * B, 8 * B, bar);
+  };
+  // The description of tile i; with it the query rows if it begins a segment.
+  auto next_tile = [&](int i) {
+    const int used = max(i - 1, 0);    // the tile before is still being worked on
+    if (i == walk.described) {
+      look_ahead(used);
+      walk.end(pp, ring, ring_s, ntiles, lane);
+      look_ahead(used);
     }
-    ++cur_k;
-    ++issued;
+    return ring[i & (kF8Ring - 1)];
+  };
+  auto copy_q = [&](int i, const Fp8Tile &t) {
+    if (!(t.head_flags & TF_FIRST)) return;
+    const int64_t row = (int64_t)ring_s[i & (kF8Ring - 1)] * p.num_q_heads +
+                        (int64_t)(t.head_flags >> 8) * G;
+    for (int k = lane; k < qbytes / 16; k += 32)
+      copy16_async(qbuf + k * 16, p.q + row * (D * 2) + k * 16, stream_policy);
   };
 
-  const int pre = ntiles < nstage ? (int)ntiles : nstage;
-  for (int k = 0; k < pre; ++k) issue(k);
+  Fp8Tile ti = next_tile(0);
+  copy_q(0, ti);
+  copy_tile(0, ti);
+  copy_commit();
+  copy_tile(1, ti);
+  copy_commit();
 
-  // ---- consume
-  Fp8Path<D, NT> st;
-  st.reset();
+  Fp8Path<D, NT, HPL> st;
+  st.init(lane);
   bool seg_from0 = false;
-  int seg_index = 0, stage = 0;
-  uint32_t parity = 0;
-  for (long long i = 0; i < ntiles; ++i) {
-    if (!mbar_wait_bounded(&bars[stage], parity, p.wait_ns)) {
-      if (lane == 0) flag_error(PA_DEVERR_TIMEOUT);
-      // copies still in flight, this tile's and later ones, land before the
-      // warp leaves
-      for (long long k = i; k < issued; ++k)
-        mbar_wait_bounded(&bars[k % nstage], (uint32_t)((k / nstage) & 1), kDrainLimitNs);
-      return;
-    }
-    const Fp8Tile ti = info[stage];
-    if (ti.flags & TF_FIRST) {
+  int seg_index = 0;
+  for (int i = 0; i < ntiles; ++i) {
+    const Fp8Tile tn = i + 1 < ntiles ? next_tile(i + 1) : ti;
+    copy_wait<1>();              // this tile's K; its V may still be on its way
+    __syncwarp();
+    if (ti.head_flags & TF_FIRST) {
       st.reset();
-      st.load_q(qslots + (size_t)stage * qbytes, G, pp.q_bf16 != 0, p.scale_log2, lane);
-      seg_from0 = (ti.flags & TF_J0) != 0;
+      st.load_q(qbuf, G, pp.q_bf16 != 0, p.scale_log2, lane);
+      seg_from0 = (ti.head_flags & TF_J0) != 0;
     }
-    if (ti.live) {
-      const uint32_t kb = smem_addr(stages + (size_t)stage * STAGE);
-      st.tile(kb, kb + TILE, smem_addr(scales + (size_t)stage * kF8ScaleBytes), B, ti.live, lane);
+    st.scores(kbuf, ksc, lane);
+    __syncwarp();                // every lane has read K (and q) before the next ones come
+    if (i + 1 < ntiles) {
+      copy_q(i + 1, tn);
+      copy_tile(0, tn);
     }
-    if (ti.flags & TF_LAST) {
-      const bool complete = seg_from0 && (ti.flags & TF_JEND);
-      st.finish(p, ti.s, ti.h, complete, (int)(2 * w + (seg_index == 0 ? 0 : 1)), lane);
+    copy_commit();
+    copy_wait<1>();              // this tile's V
+    __syncwarp();
+    if (ti.live) st.output(vbuf, vsc, ti.live, lane);
+    if (ti.head_flags & TF_LAST) {
+      const bool complete = seg_from0 && (ti.head_flags & TF_JEND);
+      st.finish(p, ring_s[i & (kF8Ring - 1)], ti.head_flags >> 8, complete,
+                (int)(2 * w + (seg_index == 0 ? 0 : 1)), lane);
       ++seg_index;
     }
     __syncwarp();
-    if (i + nstage < ntiles) issue(stage);
-    if (++stage == nstage) {
-      stage = 0;
-      parity ^= 1;
-    }
+    if (i + 1 < ntiles) copy_tile(1, tn);
+    copy_commit();
+    ti = tn;
   }
 }
 

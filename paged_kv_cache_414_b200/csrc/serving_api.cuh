@@ -136,39 +136,14 @@ int rope_and_cache(bool fp8, void *q_out, const void *q, const void *key, const 
 
 // ---------------------------------------------------------------- 8-bit decode
 
-// The code pool as rows of D bytes; a box is one (block, kv head) tile, with
-// the swizzle as wide as a row.
-bool encode_code_map(CUtensorMap *m, const void *base, long long rows, int D, int B) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)D};
-  cuuint32_t box[2] = {(cuuint32_t)D, (cuuint32_t)B};
-  cuuint32_t estr[2] = {1u, 1u};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-template <int D, int NT>
-int launch_decode_fp8(pa::DecodeFp8Params &p, const CUtensorMap &kmap, const CUtensorMap &vmap,
-                      uint8_t *workspace, size_t workspace_bytes, int dev, int sms,
-                      cudaStream_t stream) {
-  auto kern = pa::paged_decode_fp8_kernel<D, NT, kWarpsPerCta>;
+template <int D, int NT, int HPL>
+int launch_decode_fp8(pa::DecodeFp8Params &p, uint8_t *workspace, size_t workspace_bytes, int dev,
+                      int sms, cudaStream_t stream) {
+  auto kern = pa::paged_decode_fp8_kernel<D, NT, HPL, kWarpsPerCta>;
   const int G = p.d.group;
-  const size_t per_stage = (size_t)kWarpsPerCta * (pa::fp8_stage_bytes(D) + pa::kF8ScaleBytes +
-                                                   (size_t)G * D * 2 + sizeof(pa::Fp8Tile) +
-                                                   sizeof(uint64_t));
-  int ctas = NT == 1 ? 3 : 2;
-  const size_t budget = 228 * 1024;
-  auto stages_for = [&](int c) { return (int)((budget / c - 2304) / per_stage); };
-  int nst = std::min(stages_for(ctas), 4);
-  if (const int want = g_tune_ctas.load()) ctas = std::min(want, NT == 1 ? 3 : 2);
-  nst = std::min(stages_for(ctas), 4);
-  if (const int want = g_tune_nstage.load()) nst = std::min(stages_for(ctas), want);
-  nst = std::max(nst, 1);
-  const size_t smem = 1024 + per_stage * nst;
+  const size_t smem = (size_t)kWarpsPerCta * pa::fp8_warp_bytes(D, G);
+  const int most = pa::fp8_ctas(NT, HPL), want = g_tune_ctas.load();
+  const int ctas = want > 0 ? std::min(want, most) : most;
   static std::atomic<size_t> attr_set[kMaxDevices];
   if (attr_set[dev].load() < smem) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
@@ -182,11 +157,9 @@ int launch_decode_fp8(pa::DecodeFp8Params &p, const CUtensorMap &kmap, const CUt
   p.d.meta = reinterpret_cast<long long *>(workspace);
   p.d.part_ml = reinterpret_cast<float *>(workspace + off_ml);
   p.d.part_o = reinterpret_cast<float *>(workspace + off_o);
-  p.d.nstage = nst;
   const int mt = g_tune_min_tiles.load();
   p.d.min_tiles = mt > 0 ? mt : 4;
-  if (launch_dependent(kern, dim3(grid), kWarpsPerCta * 32, smem, stream, kmap, vmap, p) !=
-      cudaSuccess)
+  if (launch_dependent(kern, dim3(grid), kWarpsPerCta * 32, smem, stream, p) != cudaSuccess)
     return PA_ERR_CUDA;
   // the split merge of the 16-bit kernel: one warp per boundary and head group
   cudaError_t e;
@@ -200,6 +173,13 @@ int launch_decode_fp8(pa::DecodeFp8Params &p, const CUtensorMap &kmap, const CUt
                          p.d, w_total, hc);
   }
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+template <int D, typename... Args>
+int dispatch_decode_fp8(pa::DecodeFp8Params &p, Args... args) {
+  if (p.d.group <= 4) return launch_decode_fp8<D, 1, 1>(p, args...);
+  if (p.d.group <= 8) return launch_decode_fp8<D, 1, 2>(p, args...);
+  return launch_decode_fp8<D, 2, 2>(p, args...);
 }
 
 // ---------------------------------------------------------------- packed prompts
@@ -349,11 +329,6 @@ int pa_paged_decode_attention_fp8(float *out, const void *q, const void *k_cache
   if (current_device(&dev) != PA_OK || dev >= kMaxDevices) return PA_ERR_CUDA;
   const int sms = sm_count(dev);
   if (sms <= 0) return PA_ERR_CUDA;
-  CUtensorMap kmap, vmap;
-  const long long rows = (long long)num_blocks * num_kv_heads * block_size;
-  if (!encode_code_map(&kmap, k_cache, rows, head_dim, block_size) ||
-      !encode_code_map(&vmap, v_cache, rows, head_dim, block_size))
-    return PA_ERR_CUDA;
   pa::DecodeFp8Params p = {};
   p.d.out = out;
   p.d.q = static_cast<const uint8_t *>(q);
@@ -368,19 +343,17 @@ int pa_paged_decode_attention_fp8(float *out, const void *q, const void *k_cache
   p.d.max_blocks = (int)(((long long)max_blocks_per_seq * block_size + pa::kF8Tile - 1) /
                          pa::kF8Tile);
   p.d.num_blocks = num_blocks;
-  p.d.wait_ns = g_wait_limit_ns.load();
+  p.k_cache = static_cast<const uint8_t *>(k_cache);
+  p.v_cache = static_cast<const uint8_t *>(v_cache);
   p.kv_scale = kv_scale;
   p.table_blocks = max_blocks_per_seq;
   p.block_size = block_size;
   p.q_bf16 = dtype == PA_BF16;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   cudaStream_t st = (cudaStream_t)stream;
-  const bool wide = p.d.group > 8;
-  if (head_dim == 128)
-    return wide ? launch_decode_fp8<128, 2>(p, kmap, vmap, ws, workspace_bytes, dev, sms, st)
-                : launch_decode_fp8<128, 1>(p, kmap, vmap, ws, workspace_bytes, dev, sms, st);
-  return wide ? launch_decode_fp8<64, 2>(p, kmap, vmap, ws, workspace_bytes, dev, sms, st)
-              : launch_decode_fp8<64, 1>(p, kmap, vmap, ws, workspace_bytes, dev, sms, st);
+  return head_dim == 128
+             ? dispatch_decode_fp8<128>(p, ws, workspace_bytes, dev, sms, st)
+             : dispatch_decode_fp8<64>(p, ws, workspace_bytes, dev, sms, st);
 }
 
 int pa_copy_blocks_fp8(void *k_cache, void *v_cache, float *kv_scale, const int64_t *block_mapping,
