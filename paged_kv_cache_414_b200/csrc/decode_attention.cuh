@@ -601,21 +601,14 @@ __device__ void cta_plan(const DecodeParams &p, long long w_total, Query query, 
     }
     set_ranges(tot);
     long long cum = before_warp + incl - mine;   // blocks before sequence sbeg
-    long long u0s[NW];                           // one lane each, so one division per warp
-    {
-      const long long mine_u0 = warp_u0(lane % NW);
-#pragma unroll
-      for (int kk = 0; kk < NW; ++kk) u0s[kk] = __shfl_sync(0xffffffffu, mine_u0, kk);
-    }
 #pragma unroll
     for (int k = 0; k < KMAX; ++k) {
       if (k < K && sbeg + k < S) {
         const int nb = ceil_div_i(Lr[k], B);
         if (nb > 0) {
           const long long lo = cum * Hkv, hi = (cum + nb) * Hkv;
-#pragma unroll
           for (int kk = 0; kk < NW; ++kk) {
-            const long long uk = u0s[kk];
+            const long long uk = warp_u0(kk);
             if (uk >= lo && uk < hi) {
               loc_s[kk] = sbeg + k;
               loc_base[kk] = lo;

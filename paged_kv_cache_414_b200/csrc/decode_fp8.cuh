@@ -6,18 +6,22 @@
 // The scales never touch the codes: ks_t multiplies the finished score and
 // vs_t the weight, so both products run on the codes as they lie in the pool.
 //
-// Work split, launch plan and split merge are those of the 16-bit decode
-// kernel (decode_attention.cuh): the tiles of all (sequence, kv head) pairs,
-// numbered in order, are cut into equal contiguous ranges, one per warp, and
-// cut segments leave partials for the merge kernel.  Here a tile is 32 tokens
+// Work split as in the 16-bit decode kernel (decode_attention.cuh): the tiles of
+// all (sequence, kv head) pairs, numbered in order, are cut into equal
+// contiguous ranges, one per warp, and cut segments leave partials for the
+// merge kernel.  Every warp finds its range by itself.  Here a tile is 32 tokens
 // whatever the block size (two blocks of 16 or one of 32): half the bytes per
-// token would otherwise leave twice the bookkeeping per byte.
+// token would otherwise leave twice the bookkeeping per byte.  Every kv head of
+// a sequence begins with a tile of no tokens that stands for what a segment
+// costs besides its tiles (its query rows, its output): short sequences would
+// otherwise make some warps' equal shares take a quarter longer than the mean.
 //
-// A warp has one buffer for K and one for V, filled by 16-byte asynchronous
-// copies: the next tile's K is asked for as soon as the scores are made, its V
-// after P.V, so either is on its way during about half of a tile's work, and 8
-// to 16 warps per SM cover for each other.  (Bulk tensor copies, six of them a
-// tile, took 1400 of a warp's 5900 cycles per tile to issue.)
+// A warp has one buffer for K and one for V, filled by tensor copies: the next
+// tile's K is asked for as soon as the scores are made, its V after P.V, so
+// either is on its way during about half of a tile's work, and 8 to 16 warps
+// per SM cover for each other.  One elected lane issues, from warp-uniform
+// values; six lanes with a copy each took 1400 of a warp's 5900 cycles per
+// tile, and 16-byte asynchronous copies by all lanes the same.
 //
 // Arithmetic.
 //   * Codes become fp16 exactly (cvt.rn.f16x2.e4m3x2) and both products are
@@ -56,14 +60,34 @@ namespace pa {
 
 constexpr int kF8Tile = 32;   // tokens per tile
 
+// Tiles of a kv head of a sequence of L tokens: the empty first one, then its
+// tokens 32 at a time.
+__device__ __forceinline__ int fp8_tiles(int L) {
+  return L > 0 ? (L + kF8Tile - 1) / kF8Tile + 1 : 0;
+}
+
 struct DecodeFp8Params {
-  DecodeParams d;             // max_blocks counts tiles of 32 tokens here
-  const uint8_t *k_cache, *v_cache;
-  const float *kv_scale;
-  int table_blocks;           // blocks per row of the block table
-  int block_size;
+  float *out;                    // [S, Hq, D]
+  const uint8_t *q;              // [S, Hq, D], 16 bits
+  const float *kv_scale;         // [NB, Hkv, 2, B]
+  const int32_t *block_tables;   // [S, max_blocks]
+  const int32_t *context_lens;   // [S]
+  int4 *meta;                    // [w_total]: the segment each range begins in, for the merge
+  float2 *part_ml;               // [2 w_total][G]  (max in log2 units, sum)
+  float *part_o;                 // [2 w_total][G][D]
+  float scale_log2;              // scale * log2(e)
+  int num_seqs, num_q_heads, num_kv_heads, group;
+  int max_blocks, num_blocks, block_size;
   int q_bf16;
+  int min_tiles;                 // fewest tiles a warp is given
+  uint64_t wait_ns;              // limit of a wait on a copy before giving up (2 s by default)
 };
+
+// Length of sequence s, cut to what its row of the block table can hold.
+__device__ __forceinline__ int fp8_length(const DecodeFp8Params &p, int s) {
+  const int L = __ldg(p.context_lens + s);
+  return max(0, min(L, p.max_blocks * p.block_size));
+}
 
 // A packed pair of e4m3 codes (low 16 bits) as a packed pair of fp16 values.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x) {
@@ -90,16 +114,12 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-// 16 bytes global -> shared, asynchronously, and the groups they complete in.
-__device__ __forceinline__ void copy16_async(void *dst, const void *src, uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)),
-               "l"(reinterpret_cast<uint64_t>(src)), "l"(policy)
-               : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {   // all but this thread's last N groups have landed
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// One lane of a fully active warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(e));
+  return e != 0;
 }
 
 __device__ __forceinline__ void st_global_hint4(float *dst, float4 v, uint64_t policy) {
@@ -177,7 +197,7 @@ struct Fp8Path {
     for (int n = 0; n < NT; ++n) {
       const int head = HPL == 1 ? n * 4 + (g >> 1) : n * 8 + g;
       uint32_t raw[2 * W];
-      uint32_t top = 0;
+      uint32_t top = 0;               // the largest magnitude, as 16 bits
       const uint4 *row = reinterpret_cast<const uint4 *>(q + (size_t)head * (D * 2) + c * (D / 2));
 #pragma unroll
       for (int i = 0; i < W / 2; ++i) {
@@ -185,13 +205,12 @@ struct Fp8Path {
         raw[4 * i] = v.x, raw[4 * i + 1] = v.y, raw[4 * i + 2] = v.z, raw[4 * i + 3] = v.w;
       }
 #pragma unroll
-      for (int i = 0; i < 2 * W; ++i) {
-        const float2 f = bf16 ? Mma<__nv_bfloat16>::unpack(raw[i]) : Mma<__half>::unpack(raw[i]);
-        top = max(top, max(__float_as_uint(fabsf(f.x)), __float_as_uint(fabsf(f.y))));
-      }
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int e = scale_field(top);
+      for (int i = 0; i < 2 * W; ++i) top = __vmaxu2(top, raw[i] & 0x7fff7fffu);
+      top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      top = max(top & 0xffffu, top >> 16);
+      const float big = bf16 ? __uint_as_float(top << 16) : __half2float(__ushort_as_half(top));
+      const int e = scale_field(__float_as_uint(big));
       const float up = pow2_field(268 - e);
       const float down = pow2_field(e - 14) * scale_log2;
 #pragma unroll
@@ -207,8 +226,9 @@ struct Fp8Path {
 
   float sc[2][NT][2][HPL];     // scores of tokens 16 t + g + 8 x
 
-  // Scores of one tile, S^T[token][head]: K codes at kb, their scales at ksc.
-  __device__ __forceinline__ void scores(const uint8_t *kb, const float *ksc, int lane) {
+  // Scores of one tile, S^T[token][head]: K codes at kb, scales at sb ([block][K
+  // or V][B]).
+  __device__ __forceinline__ void scores(const uint8_t *kb, const float *sb, int B, int lane) {
     const int g = lane >> 2;
     const float zero[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -232,7 +252,7 @@ struct Fp8Path {
       }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const float ks = ksc[16 * t + g + 8 * x];
+        const float ks = sb[t * (512 / B) + g + 8 * x];   // token 16: the next block, or this one
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -241,21 +261,22 @@ struct Fp8Path {
     }
   }
 
-  // The same tile's part of the output: V codes at vb, their scales at vsc,
-  // `live` the tokens that count.
-  __device__ __forceinline__ void output(const uint8_t *vb, const float *vsc, uint32_t live,
+  // The same tile's part of the output: V codes at vb, `live` the tokens that
+  // count.
+  __device__ __forceinline__ void output(const uint8_t *vb, const float *sb, int B, uint32_t live,
                                          int lane) {
     const int g = lane >> 2, c = lane & 3;
     const float zero[4] = {0.f, 0.f, 0.f, 0.f};
     float vs[2][2];
-    const uint32_t bits = (live >> lane) & 1 ? __float_as_uint(fabsf(vsc[lane])) : 0u;
+    const float mine = sb[(lane < B ? B : 2 * B) + lane];       // V scale of token `lane`
+    const uint32_t bits = (live >> lane) & 1 ? __float_as_uint(fabsf(mine)) : 0u;
     const int top = scale_field(__reduce_max_sync(0xffffffffu, bits));
     const float up = pow2_field(268 - top);
     const float vdown = pow2_field(top - 14);   // 2^-shift of the weights
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) vs[t][x] = vsc[16 * t + g + 8 * x] * up;
+      for (int x = 0; x < 2; ++x) vs[t][x] = sb[t * (512 / B) + B + g + 8 * x] * up;
     if (live != 0xffffffffu) {                  // tokens that do not count
       const uint32_t mask = live >> g;
 #pragma unroll
@@ -368,7 +389,7 @@ struct Fp8Path {
   }
 
   // Write the segment: normalised output, or a partial for the merge.
-  __device__ __forceinline__ void finish(const DecodeParams &p, int s, int h, bool complete,
+  __device__ __forceinline__ void finish(const DecodeFp8Params &p, int s, int h, bool complete,
                                          int slot, int lane) {
     const int g = lane >> 2, c = lane & 3;
     const int G = p.group;
@@ -397,15 +418,13 @@ struct Fp8Path {
             st_global_hint4(dst + 2 * a, v, pol);
         }
         if (!complete && g == 0) {
-          float *pm = p.part_ml + ((int64_t)slot * G + head) * 2;
-          st_global_hint(pm, m[n][e], pol);
-          st_global_hint(pm + 1, lt, pol);
+          p.part_ml[(int64_t)slot * G + head] = make_float2(m[n][e], lt);
         }
       }
   }
 };
 
-// A tile as its warp's ring holds it: rows of its tokens 0 and 16 in the code
+// A tile as its warp's ring holds it: first rows of its blocks in the code
 // pools (-1: no such block), the tokens that count, TF_ flags and kv head << 8.
 struct Fp8Tile {
   int row0, row1;
@@ -424,30 +443,30 @@ struct Fp8Walk {
   int id0, id1, my_h, my_j;  // this lane's tile of them
 
   __device__ __forceinline__ void begin(const DecodeFp8Params &p, int ntiles, int lane) {
-    while (h >= p.d.num_kv_heads || nt == 0) {   // next sequence with tiles
+    while (h >= p.num_kv_heads || nt == 0) {   // next sequence with tiles
       h = 0;
       j = 0;
-      if (s + 1 >= p.d.num_seqs) {   // only if lengths changed under the kernel: empty tiles
+      if (s + 1 >= p.num_seqs) {   // only if lengths changed under the kernel: empty tiles
         L = 0;
         nt = 1;
         break;
       }
       ++s;
-      L = seq_len_clamped<kF8Tile>(p.d, s);
-      nt = ceil_div_i(L, kF8Tile);
+      L = fp8_length(p, s);
+      nt = fp8_tiles(L);
     }
-    const int64_t left = (int64_t)(p.d.num_kv_heads - h) * nt - j;
+    const int64_t left = (int64_t)(p.num_kv_heads - h) * nt - j;
     n = min((int)min(left, (int64_t)32), ntiles - described);
     my_h = h;
     my_j = j + lane;                 // a few steps, one when nt >= 32
     while (my_j >= nt) my_j -= nt, ++my_h;
     id0 = id1 = -1;
     if (lane < n) {
-      const int per = kF8Tile / p.block_size, b0 = my_j * per;
-      const int32_t *table = p.d.block_tables + (int64_t)s * p.table_blocks + b0;
-      const bool two = per == 2 && L - my_j * kF8Tile > p.block_size;
-      if (b0 < p.table_blocks) id0 = __ldg(table);
-      if (two && b0 + 1 < p.table_blocks) id1 = __ldg(table + 1);
+      const int per = kF8Tile / p.block_size, b0 = (my_j - 1) * per;
+      const int32_t *table = p.block_tables + (int64_t)s * p.max_blocks + b0;
+      const bool two = per == 2 && L - (my_j - 1) * kF8Tile > p.block_size;
+      if (my_j > 0 && b0 < p.max_blocks) id0 = __ldg(table);
+      if (my_j > 0 && two && b0 + 1 < p.max_blocks) id1 = __ldg(table + 1);
     }
   }
 
@@ -455,21 +474,20 @@ struct Fp8Walk {
                                       int ntiles, int lane) {
     if (lane < n) {
       const int B = p.block_size, per = kF8Tile / B;
-      const int len = min(kF8Tile, L - my_j * kF8Tile);
+      const int len = my_j == 0 ? 0 : min(kF8Tile, L - (my_j - 1) * kF8Tile);
       const uint32_t below = len == 32 ? 0xffffffffu : (1u << len) - 1u;
-      const bool in0 = id0 >= 0 && id0 < p.d.num_blocks, in1 = id1 >= 0 && id1 < p.d.num_blocks;
+      const bool in0 = id0 >= 0 && id0 < p.num_blocks, in1 = id1 >= 0 && id1 < p.num_blocks;
       const bool first = my_j == 0, last = my_j == nt - 1;
       const int at = described + lane;
       Fp8Tile t;
-      t.row0 = in0 ? (id0 * p.d.num_kv_heads + my_h) * B : -1;
-      t.row1 = per == 1 ? (in0 ? t.row0 + 16 : -1)
-                        : (in1 ? (id1 * p.d.num_kv_heads + my_h) * B : -1);
+      t.row0 = in0 ? (id0 * p.num_kv_heads + my_h) * B : -1;
+      t.row1 = in1 ? (id1 * p.num_kv_heads + my_h) * B : -1;
       t.live = below & ((in0 ? (per == 2 ? 0x0000ffffu : 0xffffffffu) : 0u) |
                         (in1 ? 0xffff0000u : 0u));
       t.head_flags = (my_h << 8) | (first || at == 0 ? TF_FIRST : 0) | (first ? TF_J0 : 0) |
                      (last || at == ntiles - 1 ? TF_LAST : 0) | (last ? TF_JEND : 0);
       if (t.live != below)           // a block outside the pool, or past the table's end
-        flag_error(my_j * per + (in0 ? 1 : 0) >= p.table_blocks ? PA_DEVERR_CONTEXT_LEN
+        flag_error((my_j - 1) * per + (in0 ? 1 : 0) >= p.max_blocks ? PA_DEVERR_CONTEXT_LEN
                                                                 : PA_DEVERR_BLOCK_ID);
       ring[at & (kF8Ring - 1)] = t;
       ring_s[at & (kF8Ring - 1)] = s;
@@ -484,10 +502,13 @@ struct Fp8Walk {
   }
 };
 
-// Smem of one warp: a K and a V tile, their scales, the group's query rows, a
-// ring of tile descriptions.
+// Smem of one warp: a K and a V tile, two tiles' scales, the group's query
+// rows, a ring of tile descriptions, two barriers; in whole swizzle atoms.
+constexpr int kF8ScaleFloats = 2 * kF8Tile;
 __host__ __device__ constexpr int fp8_warp_bytes(int D, int G) {
-  return 2 * kF8Tile * D + 2 * kF8Tile * 4 + G * D * 2 + kF8Ring * (int)(sizeof(Fp8Tile) + 4);
+  return (2 * kF8Tile * D + 2 * kF8ScaleFloats * 4 + G * D * 2 +
+          kF8Ring * (int)(sizeof(Fp8Tile) + 4) + 16 + 1023) /
+         1024 * 1024;
 }
 
 // CTAs per SM that registers allow.
@@ -495,140 +516,185 @@ __host__ __device__ constexpr int fp8_ctas(int NT, int HPL) {
   return NT * HPL == 1 ? 4 : (NT * HPL == 2 ? 3 : 2);
 }
 
+// Sum over the lanes before this one, and over all of them.
+__device__ __forceinline__ int warp_scan(int v, int lane, int *total) {
+  int incl = v;
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, x);
+    if (lane >= x) incl += y;
+  }
+  *total = __shfl_sync(0xffffffffu, incl, 31);
+  return incl - v;
+}
+
 template <int D, int NT, int HPL, int NW>
 __global__ void __launch_bounds__(NW * 32, fp8_ctas(NT, HPL))
-    paged_decode_fp8_kernel(const DecodeFp8Params pp) {
+    paged_decode_fp8_kernel(const __grid_constant__ CUtensorMap kmap,
+                            const __grid_constant__ CUtensorMap vmap, const DecodeFp8Params p) {
   constexpr int TILE = kF8Tile * D;
-  const DecodeParams &p = pp.d;
-  const int G = p.group, B = pp.block_size;
+  const int G = p.group, B = p.block_size, S = p.num_seqs;
   const int qbytes = G * D * 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  extern __shared__ __align__(128) uint8_t smem_raw[];
-  uint8_t *kbuf = smem_raw + (size_t)warp * fp8_warp_bytes(D, G), *vbuf = kbuf + TILE;
-  float *ksc = reinterpret_cast<float *>(vbuf + TILE), *vsc = ksc + kF8Tile;
-  uint8_t *qbuf = reinterpret_cast<uint8_t *>(vsc + kF8Tile);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *kbuf = smem + (size_t)warp * fp8_warp_bytes(D, G), *vbuf = kbuf + TILE;
+  float *scales = reinterpret_cast<float *>(vbuf + TILE);
+  uint8_t *qbuf = reinterpret_cast<uint8_t *>(scales + 2 * kF8ScaleFloats);
   Fp8Tile *ring = reinterpret_cast<Fp8Tile *>(qbuf + qbytes);
   int *ring_s = reinterpret_cast<int *>(ring + kF8Ring);
+  uint64_t *kbar = reinterpret_cast<uint64_t *>(ring_s + kF8Ring), *vbar = kbar + 1;
 
-  __shared__ long long red[NW];
-  __shared__ int loc_s[NW];
-  __shared__ long long loc_base[NW];
-  __shared__ int loc_L[NW];
-
+  if (lane == 0) {
+    mbar_init(kbar, 1);
+    mbar_init(vbar, 1);
+    fence_barrier_init();
+  }
+  if (threadIdx.x == 0) {
+    prefetch_tensormap(&kmap);
+    prefetch_tensormap(&vmap);
+  }
   grid_dependency_wait();
   allow_dependent_launch();
 
-  // ---- plan: total tiles, this CTA's warp ranges
-  const long long w_total = (long long)gridDim.x * NW;
-  const long long w = (long long)blockIdx.x * NW + warp;
-  long long U = 0, w_active = 0;
-  cta_plan<kF8Tile, NW>(
-      p, w_total, [&](int k, long long U_, long long wa_) -> long long {
-        const long long wk = (long long)blockIdx.x * NW + k;
-        return wk < wa_ ? (wk * U_) / wa_ : -1;
-      },
-      true, red, loc_s, loc_base, loc_L, U, w_active);
-  const bool active = w < w_active;
-  const long long u0 = active ? (w * U) / w_active : 0;
-  const long long u1 = active ? ((w + 1) * U) / w_active : 0;
-  long long *meta = p.meta + w * kMetaWords;
-  if (!active) {
-    if (lane < kMetaWords) meta[lane] = lane == 3 ? U : (lane == 4 ? w_active : 0);
+  // ---- this warp's range: lane l counts the tiles (of one kv head) of
+  // sequences per * l ..
+  const int w_total = gridDim.x * NW, w = blockIdx.x * NW + warp;
+  const int per = (S + 31) / 32;
+  int mine = 0;
+#pragma unroll 8
+  for (int k = 0; k < per; ++k) {
+    const int s = lane * per + k;
+    mine += s < S ? fp8_tiles(fp8_length(p, s)) : 0;
+  }
+  int total;
+  const int before = warp_scan(mine, lane, &total);
+  const long long U = (long long)total * p.num_kv_heads;
+  const int w_active = (int)min((long long)w_total, (U + p.min_tiles - 1) / p.min_tiles);
+  // empty sequences' rows, and lengths that the table cannot hold
+  for (int s = w; s < S; s += w_total) {
+    const int L = __ldg(p.context_lens + s);
+    if (lane == 0 && (L < 0 || L > p.max_blocks * B)) flag_error(PA_DEVERR_CONTEXT_LEN);
+    if (L <= 0 || p.max_blocks == 0) {
+      float4 *row = reinterpret_cast<float4 *>(p.out + (int64_t)s * p.num_q_heads * D);
+      for (int k = lane; k < p.num_q_heads * D / 4; k += 32) row[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+  if (w >= w_active) {
+    if (lane == 0) p.meta[w] = make_int4(0, 0, 0, 0);
     return;
   }
-
-  // ---- this warp's first tile
-  const int s0 = loc_s[warp];
-  const long long base0 = loc_base[warp];
-  const int L0 = loc_L[warp];
-  const int nt0 = ceil_div_i(L0, kF8Tile);
-  const long long r0 = u0 - base0;
-  const int h0 = (int)(r0 / nt0);
-  const int j0 = (int)(r0 - (long long)h0 * nt0);
-  if (lane < kMetaWords) {   // descriptor for the merge, as in the 16-bit kernel
-    const long long seg_lo = base0 + (long long)h0 * nt0;
-    long long v = 1;
-    switch (lane) {
-      case 0: v = u0; break;
-      case 1: v = seg_lo; break;
-      case 2: v = seg_lo + nt0; break;
-      case 3: v = U; break;
-      case 4: v = w_active; break;
-      case 5: v = s0; break;
-      case 6: v = h0; break;
-      default: v = 1;
-    }
-    meta[lane] = v;
-  }
+  const long long u01 = (long long)(w + (lane & 1)) * U / w_active;
+  const long long u0 = __shfl_sync(0xffffffffu, u01, 0), u1 = __shfl_sync(0xffffffffu, u01, 1);
   const int ntiles = (int)(u1 - u0);
+  // the sequence that tile u0 belongs to: first the lane that counted it, then
+  // that lane's sequences 32 at a time
+  const int t0 = (int)(u0 / p.num_kv_heads);
+  const int owner =
+      31 - __clz(__ballot_sync(0xffffffffu, before <= t0));   // the last one that begins before
+  int s0 = owner * per, base = __shfl_sync(0xffffffffu, before, owner), L0 = 0;
+  for (int k0 = 0; k0 < per; k0 += 32) {
+    const int s = owner * per + k0 + lane;
+    const int L = k0 + lane < per && s < S ? fp8_length(p, s) : 0;
+    int sum;
+    const int at = base + warp_scan(fp8_tiles(L), lane, &sum);
+    if (base + sum <= t0) {
+      base += sum;
+      continue;
+    }
+    const int hit = 31 - __clz(__ballot_sync(0xffffffffu, at <= t0));
+    s0 = owner * per + k0 + hit;
+    base = __shfl_sync(0xffffffffu, at, hit);
+    L0 = __shfl_sync(0xffffffffu, L, hit);
+    break;
+  }
+  const int nt0 = fp8_tiles(L0);
+  const long long r0 = u0 - (long long)base * p.num_kv_heads;
+  const int h0 = (int)(r0 / nt0), j0 = (int)(r0 - (long long)h0 * nt0);
 
   // ---- the walk, and the copies of a tile
   Fp8Walk walk;
   walk.s = s0, walk.L = L0, walk.nt = nt0, walk.h = h0, walk.j = j0;
   walk.described = 0;
-  walk.begin(pp, ntiles, lane);
-  walk.end(pp, ring, ring_s, ntiles, lane);
+  walk.begin(p, ntiles, lane);
+  walk.end(p, ring, ring_s, ntiles, lane);
   // the next run, if the ring has room for it: its block ids travel meanwhile
   auto look_ahead = [&](int consumed) {
     if (walk.n == 0 && walk.described < ntiles && walk.described - consumed <= kF8Ring - 32)
-      walk.begin(pp, ntiles, lane);
+      walk.begin(p, ntiles, lane);
   };
   look_ahead(0);
 
   const uint64_t stream_policy = l2_policy_evict_first();
-  // chunk 32 i + lane of a tile: D / 16 a row, swizzled within the row
-  constexpr int CPR = D / 16, COPIES = kF8Tile * D / 512;
-  const int crow = lane / CPR, cch = lane % CPR;
-  const int dst0 = crow * D + ((D == 128 ? cch ^ crow : cch ^ ((crow >> 1) & 3)) << 4);
-  // K (which = 0) or V of tile i, and their scales
-  auto copy_tile = [&](int which, const Fp8Tile &t) {
-    const uint8_t *pool = (which ? pp.v_cache : pp.k_cache) + lane * 16;
-    uint8_t *dst = which ? vbuf : kbuf;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int row = half ? t.row1 : t.row0;
-      if (row < 0) continue;
-      const uint8_t *src = pool + (int64_t)row * D;
-#pragma unroll
-      for (int i = 0; i < COPIES / 2; ++i) {
-        // (i's part of the row number is a multiple of 4 for D = 128, of 8 for 64)
-        const int at = (half * COPIES / 2 + i) * 512;
-        copy16_async(dst + at + (D == 128 ? dst0 ^ ((i & 1) << 6) : dst0), src + i * 512,
-                     stream_policy);
+  // K, scales and, where a segment begins, query rows of tile i
+  auto copy_k = [&](int i, const Fp8Tile &t) {
+    const int row0 = __shfl_sync(0xffffffffu, t.row0, 0);
+    const int row1 = __shfl_sync(0xffffffffu, t.row1, 0);
+    const bool first = __shfl_sync(0xffffffffu, t.head_flags, 0) & TF_FIRST;
+    float *sc = scales + (i & 1) * kF8ScaleFloats;
+    fence_proxy_async_smem();      // this lane's reads of the buffers, before copies into them
+    __syncwarp();
+    if (elect_one()) {
+      mbar_arrive_expect_tx(kbar, ((row0 >= 0) + (row1 >= 0)) * (B * D + 8 * B) +
+                                      (first ? (uint32_t)qbytes : 0u));
+      if (row0 >= 0) {
+        tma_load_2d_hint(kbuf, &kmap, 0, row0, kbar, stream_policy);
+        bulk_load(sc, p.kv_scale + (int64_t)row0 * 2, 8 * B, kbar);
       }
-      if ((lane >> 2) == half) {
-        const int64_t first =
-            B == 16 ? (int64_t)row * 2 + which * 16 : (int64_t)t.row0 * 2 + which * 32 + half * 16;
-        copy16_async((which ? vsc : ksc) + 4 * lane, pp.kv_scale + first + 4 * (lane & 3),
-                     stream_policy);
+      if (row1 >= 0) {
+        tma_load_2d_hint(kbuf + B * D, &kmap, 0, row1, kbar, stream_policy);
+        bulk_load(sc + 2 * B, p.kv_scale + (int64_t)row1 * 2, 8 * B, kbar);
+      }
+      if (first) {
+        const int64_t row = (int64_t)ring_s[i & (kF8Ring - 1)] * p.num_q_heads +
+                            (int64_t)(t.head_flags >> 8) * G;
+        bulk_load(qbuf, p.q + row * (D * 2), qbytes, kbar);
       }
     }
   };
-  // The description of tile i; with it the query rows if it begins a segment.
+  auto copy_v = [&](const Fp8Tile &t) {
+    const int row0 = __shfl_sync(0xffffffffu, t.row0, 0);
+    const int row1 = __shfl_sync(0xffffffffu, t.row1, 0);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (elect_one()) {
+      mbar_arrive_expect_tx(vbar, ((row0 >= 0) + (row1 >= 0)) * B * D);
+      if (row0 >= 0) tma_load_2d_hint(vbuf, &vmap, 0, row0, vbar, stream_policy);
+      if (row1 >= 0) tma_load_2d_hint(vbuf + B * D, &vmap, 0, row1, vbar, stream_policy);
+    }
+  };
+  // The description of tile i.
   auto next_tile = [&](int i) {
     const int used = max(i - 1, 0);    // the tile before is still being worked on
     if (i == walk.described) {
       look_ahead(used);
-      walk.end(pp, ring, ring_s, ntiles, lane);
+      walk.end(p, ring, ring_s, ntiles, lane);
       look_ahead(used);
     }
     return ring[i & (kF8Ring - 1)];
   };
-  auto copy_q = [&](int i, const Fp8Tile &t) {
-    if (!(t.head_flags & TF_FIRST)) return;
-    const int64_t row = (int64_t)ring_s[i & (kF8Ring - 1)] * p.num_q_heads +
-                        (int64_t)(t.head_flags >> 8) * G;
-    for (int k = lane; k < qbytes / 16; k += 32)
-      copy16_async(qbuf + k * 16, p.q + row * (D * 2) + k * 16, stream_policy);
-  };
-
   Fp8Tile ti = next_tile(0);
-  copy_q(0, ti);
-  copy_tile(0, ti);
-  copy_commit();
-  copy_tile(1, ti);
-  copy_commit();
+  copy_k(0, ti);
+  copy_v(ti);
+
+  // ---- for the merge, while the first copies travel: if this range begins
+  // inside a segment and no earlier one does, the segment's (sequence, kv
+  // head), its first partial and the number of them; the others are the first
+  // partials of the ranges behind the first
+  {
+    const long long lo = u0 - j0, hi = lo + nt0;
+    // the range that holds tile u: the largest c with c U / w_active <= u
+    const long long c01 = (((lane & 1) ? hi : lo + 1) * w_active - 1) / U;
+    const int c_lo = (int)__shfl_sync(0xffffffffu, c01, 0);
+    const int c_hi = (int)__shfl_sync(0xffffffffu, c01, 1);
+    const bool starts = (long long)c_lo * U / w_active == lo;   // range c_lo begins with the segment
+    const bool merge = j0 > 0 && c_lo == w - 1;
+    if (lane == 0)
+      p.meta[w] = make_int4(merge ? s0 * p.num_kv_heads + h0 : 0, 2 * c_lo + (starts ? 0 : 1),
+                            c_lo, merge ? c_hi - c_lo + 1 : 0);
+  }
 
   Fp8Path<D, NT, HPL> st;
   st.init(lane);
@@ -636,33 +702,138 @@ __global__ void __launch_bounds__(NW * 32, fp8_ctas(NT, HPL))
   int seg_index = 0;
   for (int i = 0; i < ntiles; ++i) {
     const Fp8Tile tn = i + 1 < ntiles ? next_tile(i + 1) : ti;
-    copy_wait<1>();              // this tile's K; its V may still be on its way
-    __syncwarp();
+    const float *sc = scales + (i & 1) * kF8ScaleFloats;
+    if (!mbar_wait_bounded(kbar, i & 1, p.wait_ns)) {
+      if (lane == 0) flag_error(PA_DEVERR_TIMEOUT);
+      // copies still in flight land before the warp leaves
+      mbar_wait_bounded(kbar, i & 1, kDrainLimitNs);
+      mbar_wait_bounded(vbar, i & 1, kDrainLimitNs);
+      return;
+    }
     if (ti.head_flags & TF_FIRST) {
       st.reset();
-      st.load_q(qbuf, G, pp.q_bf16 != 0, p.scale_log2, lane);
+      st.load_q(qbuf, G, p.q_bf16 != 0, p.scale_log2, lane);
       seg_from0 = (ti.head_flags & TF_J0) != 0;
     }
-    st.scores(kbuf, ksc, lane);
-    __syncwarp();                // every lane has read K (and q) before the next ones come
-    if (i + 1 < ntiles) {
-      copy_q(i + 1, tn);
-      copy_tile(0, tn);
+    if (ti.live) st.scores(kbuf, sc, B, lane);
+    if (i + 1 < ntiles) copy_k(i + 1, tn);
+    if (!mbar_wait_bounded(vbar, i & 1, p.wait_ns)) {
+      if (lane == 0) flag_error(PA_DEVERR_TIMEOUT);
+      mbar_wait_bounded(vbar, i & 1, kDrainLimitNs);
+      if (i + 1 < ntiles) mbar_wait_bounded(kbar, (i + 1) & 1, kDrainLimitNs);
+      return;
     }
-    copy_commit();
-    copy_wait<1>();              // this tile's V
-    __syncwarp();
-    if (ti.live) st.output(vbuf, vsc, ti.live, lane);
+    if (ti.live) st.output(vbuf, sc, B, ti.live, lane);
+    if (i + 1 < ntiles) copy_v(tn);
     if (ti.head_flags & TF_LAST) {
       const bool complete = seg_from0 && (ti.head_flags & TF_JEND);
       st.finish(p, ring_s[i & (kF8Ring - 1)], ti.head_flags >> 8, complete,
-                (int)(2 * w + (seg_index == 0 ? 0 : 1)), lane);
+                2 * w + (seg_index == 0 ? 0 : 1), lane);
       ++seg_index;
     }
-    __syncwarp();
-    if (i + 1 < ntiles) copy_tile(1, tn);
-    copy_commit();
     ti = tn;
+  }
+}
+
+// ============================================================================
+// Merge of split segments.  A warp looks at `span` ranges (one per lane) and
+// merges the segments that are first cut at one of them, GMW heads at a time:
+// with many segments about every range begins inside one, with few long ones
+// a segment has many partials and the heads go to different warps.
+// ============================================================================
+template <int D, int GMW>
+__global__ void __launch_bounds__(128)
+    paged_decode_fp8_merge_kernel(const DecodeFp8Params p, int w_total, int span, int groups) {
+  constexpr int VPL = D / 32;
+  constexpr int UNR = 16 / GMW;   // partials per batch of loads
+  using VecT = typename std::conditional<VPL == 4, float4, float2>::type;
+  grid_dependency_wait();
+  const int lane = threadIdx.x & 31;
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int G = p.group, g0 = t % groups * GMW, b = t / groups * span + lane;
+  const int4 mine = lane < span && b < w_total ? __ldcg(p.meta + b) : make_int4(0, 0, 0, 0);
+  unsigned todo = __ballot_sync(0xffffffffu, mine.w > 0);
+  while (todo) {
+    const int src = __ffs(todo) - 1;
+    todo &= todo - 1;
+    const int sh = __shfl_sync(0xffffffffu, mine.x, src);
+    const int first = __shfl_sync(0xffffffffu, mine.y, src);
+    const int c_lo = __shfl_sync(0xffffffffu, mine.z, src);
+    const int n = __shfl_sync(0xffffffffu, mine.w, src);
+    float M[GMW], den[GMW], num[GMW][VPL];
+#pragma unroll
+    for (int g = 0; g < GMW; ++g) {
+      M[g] = -INFINITY;
+      den[g] = 0.f;
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) num[g][v] = 0.f;
+    }
+    for (int k0 = 0; k0 < n; k0 += 32) {
+      const int k = k0 + lane, cnt = min(n - k0, 32);
+      const bool ok = k < n;
+      const long long row = (long long)(k == 0 ? first : 2 * (c_lo + k)) * G + g0;
+      VecT buf[UNR][GMW];
+      auto fetch = [&](int j0) {
+#pragma unroll
+        for (int u = 0; u < UNR; ++u) {
+          const long long rj = __shfl_sync(0xffffffffu, row, min(j0 + u, cnt - 1));
+#pragma unroll
+          for (int g = 0; g < GMW; ++g)
+            buf[u][g] = __ldcg(reinterpret_cast<const VecT *>(
+                p.part_o + (rj + min(g, G - 1 - g0)) * D + lane * VPL));
+        }
+      };
+      float2 ml[GMW];
+#pragma unroll
+      for (int g = 0; g < GMW; ++g)
+        ml[g] = ok ? __ldcg(p.part_ml + row + min(g, G - 1 - g0)) : make_float2(-INFINITY, 0.f);
+      fetch(0);
+      float wk[GMW];
+#pragma unroll
+      for (int g = 0; g < GMW; ++g) {
+        float cm = ml[g].x;
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, x));
+        const float Mn = fmaxf(M[g], cm);
+        const float so = M[g] == -INFINITY ? 0.f : exp2f(M[g] - Mn);
+        wk[g] = ml[g].x == -INFINITY ? 0.f : exp2f(ml[g].x - Mn);
+        float dl = wk[g] * ml[g].y;
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) dl += __shfl_xor_sync(0xffffffffu, dl, x);
+        den[g] = den[g] * so + dl;
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) num[g][v] *= so;
+        M[g] = Mn;
+      }
+      for (int j0 = 0; j0 < cnt; j0 += UNR) {
+        if (j0 > 0) fetch(j0);
+#pragma unroll
+        for (int u = 0; u < UNR; ++u) {
+          if (j0 + u >= cnt) break;
+#pragma unroll
+          for (int g = 0; g < GMW; ++g) {
+            const float wj = __shfl_sync(0xffffffffu, wk[g], j0 + u);
+            num[g][0] = fmaf(wj, buf[u][g].x, num[g][0]);
+            num[g][1] = fmaf(wj, buf[u][g].y, num[g][1]);
+            if constexpr (VPL == 4) {
+              num[g][2] = fmaf(wj, buf[u][g].z, num[g][2]);
+              num[g][3] = fmaf(wj, buf[u][g].w, num[g][3]);
+            }
+          }
+        }
+      }
+    }
+    float *dst = p.out + ((int64_t)sh * G + g0) * D + lane * VPL;
+#pragma unroll
+    for (int g = 0; g < GMW; ++g) {
+      if (g0 + g >= G) break;
+      const float inv = den[g] == 0.f ? 0.f : 1.f / den[g];
+      if constexpr (VPL == 4)
+        *reinterpret_cast<float4 *>(dst + g * D) =
+            make_float4(num[g][0] * inv, num[g][1] * inv, num[g][2] * inv, num[g][3] * inv);
+      else
+        *reinterpret_cast<float2 *>(dst + g * D) = make_float2(num[g][0] * inv, num[g][1] * inv);
+    }
   }
 }
 

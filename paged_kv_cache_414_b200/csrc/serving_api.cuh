@@ -136,12 +136,28 @@ int rope_and_cache(bool fp8, void *q_out, const void *q, const void *key, const 
 
 // ---------------------------------------------------------------- 8-bit decode
 
+// The code pool as rows of D bytes; a box is one (block, kv head) tile, with
+// the swizzle as wide as a row.
+bool encode_code_map(CUtensorMap *m, const void *base, long long rows, int D, int B) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)D};
+  cuuint32_t box[2] = {(cuuint32_t)D, (cuuint32_t)B};
+  cuuint32_t estr[2] = {1u, 1u};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, int NT, int HPL>
-int launch_decode_fp8(pa::DecodeFp8Params &p, uint8_t *workspace, size_t workspace_bytes, int dev,
-                      int sms, cudaStream_t stream) {
+int launch_decode_fp8(pa::DecodeFp8Params &p, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                      uint8_t *workspace, size_t workspace_bytes, int dev, int sms,
+                      cudaStream_t stream) {
   auto kern = pa::paged_decode_fp8_kernel<D, NT, HPL, kWarpsPerCta>;
-  const int G = p.d.group;
-  const size_t smem = (size_t)kWarpsPerCta * pa::fp8_warp_bytes(D, G);
+  const int G = p.group;
+  const size_t smem = 1024 + (size_t)kWarpsPerCta * pa::fp8_warp_bytes(D, G);   // 1024: alignment
   const int most = pa::fp8_ctas(NT, HPL), want = g_tune_ctas.load();
   const int ctas = want > 0 ? std::min(want, most) : most;
   static std::atomic<size_t> attr_set[kMaxDevices];
@@ -154,31 +170,35 @@ int launch_decode_fp8(pa::DecodeFp8Params &p, uint8_t *workspace, size_t workspa
   const int grid = sms * ctas, w_total = grid * kWarpsPerCta;
   size_t off_ml, off_o;
   if (workspace_bytes < workspace_for(w_total, G, D, &off_ml, &off_o)) return PA_ERR_WORKSPACE;
-  p.d.meta = reinterpret_cast<long long *>(workspace);
-  p.d.part_ml = reinterpret_cast<float *>(workspace + off_ml);
-  p.d.part_o = reinterpret_cast<float *>(workspace + off_o);
+  p.meta = reinterpret_cast<int4 *>(workspace);
+  p.part_ml = reinterpret_cast<float2 *>(workspace + off_ml);
+  p.part_o = reinterpret_cast<float *>(workspace + off_o);
   const int mt = g_tune_min_tiles.load();
-  p.d.min_tiles = mt > 0 ? mt : 4;
-  if (launch_dependent(kern, dim3(grid), kWarpsPerCta * 32, smem, stream, p) != cudaSuccess)
+  p.min_tiles = mt > 0 ? mt : 4;
+  if (launch_dependent(kern, dim3(grid), kWarpsPerCta * 32, smem, stream, kmap, vmap, p) !=
+      cudaSuccess)
     return PA_ERR_CUDA;
-  // the split merge of the 16-bit kernel: one warp per boundary and head group
-  cudaError_t e;
-  if (G <= 4) {
-    e = launch_dependent(pa::paged_decode_merge_kernel<D, 4>, dim3((w_total - 1 + 3) / 4), 128, 0,
-                         stream, p.d, w_total, 1);
-  } else {
-    const int hc = (G + 1) / 2;
-    e = launch_dependent(pa::paged_decode_merge_kernel<D, 2>,
-                         dim3((unsigned)(((long long)(w_total - 1) * hc + 3) / 4)), 128, 0, stream,
-                         p.d, w_total, hc);
-  }
+  // Segments are at least as many as (sequence, kv head) pairs, cuts at most as
+  // many as ranges: with many pairs a warp takes one range and four heads, else
+  // as many ranges as there are to a pair, and one head.
+  const long long pairs = (long long)p.num_seqs * p.num_kv_heads;
+  int span = 1;
+  while (span < 32 && pairs * span * 2 <= w_total) span *= 2;
+  const int heads = span > 1 ? 1 : 4, groups = (G + heads - 1) / heads;
+  const long long warps = (long long)((w_total + span - 1) / span) * groups;
+  const dim3 mgrid((unsigned)((warps + 3) / 4));
+  const cudaError_t e =
+      span > 1 ? launch_dependent(pa::paged_decode_fp8_merge_kernel<D, 1>, mgrid, 128, 0, stream, p,
+                                  w_total, span, groups)
+               : launch_dependent(pa::paged_decode_fp8_merge_kernel<D, 4>, mgrid, 128, 0, stream, p,
+                                  w_total, span, groups);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 template <int D, typename... Args>
 int dispatch_decode_fp8(pa::DecodeFp8Params &p, Args... args) {
-  if (p.d.group <= 4) return launch_decode_fp8<D, 1, 1>(p, args...);
-  if (p.d.group <= 8) return launch_decode_fp8<D, 1, 2>(p, args...);
+  if (p.group <= 4) return launch_decode_fp8<D, 1, 1>(p, args...);
+  if (p.group <= 8) return launch_decode_fp8<D, 1, 2>(p, args...);
   return launch_decode_fp8<D, 2, 2>(p, args...);
 }
 
@@ -329,31 +349,32 @@ int pa_paged_decode_attention_fp8(float *out, const void *q, const void *k_cache
   if (current_device(&dev) != PA_OK || dev >= kMaxDevices) return PA_ERR_CUDA;
   const int sms = sm_count(dev);
   if (sms <= 0) return PA_ERR_CUDA;
+  CUtensorMap kmap, vmap;
+  const long long rows = (long long)num_blocks * num_kv_heads * block_size;
+  if (!encode_code_map(&kmap, k_cache, rows, head_dim, block_size) ||
+      !encode_code_map(&vmap, v_cache, rows, head_dim, block_size))
+    return PA_ERR_CUDA;
   pa::DecodeFp8Params p = {};
-  p.d.out = out;
-  p.d.q = static_cast<const uint8_t *>(q);
-  p.d.block_tables = block_tables;
-  p.d.context_lens = context_lens;
-  p.d.scale_log2 = scale * 1.4426950408889634f;
-  p.d.num_seqs = num_seqs;
-  p.d.num_q_heads = num_q_heads;
-  p.d.num_kv_heads = num_kv_heads;
-  p.d.group = num_q_heads / num_kv_heads;
-  p.d.head_dim = head_dim;
-  p.d.max_blocks = (int)(((long long)max_blocks_per_seq * block_size + pa::kF8Tile - 1) /
-                         pa::kF8Tile);
-  p.d.num_blocks = num_blocks;
-  p.k_cache = static_cast<const uint8_t *>(k_cache);
-  p.v_cache = static_cast<const uint8_t *>(v_cache);
+  p.out = out;
+  p.q = static_cast<const uint8_t *>(q);
   p.kv_scale = kv_scale;
-  p.table_blocks = max_blocks_per_seq;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.num_seqs = num_seqs;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.group = num_q_heads / num_kv_heads;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_blocks = num_blocks;
   p.block_size = block_size;
   p.q_bf16 = dtype == PA_BF16;
+  p.wait_ns = g_wait_limit_ns.load();
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   cudaStream_t st = (cudaStream_t)stream;
   return head_dim == 128
-             ? dispatch_decode_fp8<128>(p, ws, workspace_bytes, dev, sms, st)
-             : dispatch_decode_fp8<64>(p, ws, workspace_bytes, dev, sms, st);
+             ? dispatch_decode_fp8<128>(p, kmap, vmap, ws, workspace_bytes, dev, sms, st)
+             : dispatch_decode_fp8<64>(p, kmap, vmap, ws, workspace_bytes, dev, sms, st);
 }
 
 int pa_copy_blocks_fp8(void *k_cache, void *v_cache, float *kv_scale, const int64_t *block_mapping,

@@ -363,6 +363,26 @@ def test_decode_fp8_nan_and_infinite_rows_reach_their_outputs(pa):
     assert not out[1, 2:].isfinite().any() and out[1, :2].isfinite().all()
 
 
+def test_decode_fp8_wait_limit(pa):
+    """Waits that run out are reported and the next call is whole.  (270 MB of cache, more than
+    the L2 holds: a tile's copy takes longer than the work on the tile before it.)"""
+    B, Hkv, D, n = 16, 8, 128, 131072
+    k, v, sc = make_pool(n // B, Hkv, B, D, seed=21)
+    tables = make_tables([n], B, n // B, 22)
+    q = torch.randn(1, 32, D, generator=generator(23), device="cuda").half()
+    out = torch.empty(1, 32, D, device="cuda")
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    try:
+        pa.pa_set_wait_limit(1)
+        pa.pa_paged_decode_attention_fp8(out, q, k, v, sc, tables, lens, D ** -0.5, Hkv)
+        assert pa.pa_device_error(clear=True) & pa.DEVERR["timeout"]
+    finally:
+        pa.pa_set_wait_limit(0)
+    pa.pa_paged_decode_attention_fp8(out, q, k, v, sc, tables, lens, D ** -0.5, Hkv)
+    want, tol = decode_reference(q, k, v, sc, tables, [n], B, D ** -0.5)
+    assert ((out.double() - want).abs() <= tol).all()
+
+
 # ------------------------------------------------------------------ gather, copies
 
 @pytest.mark.parametrize("dtype,Hkv,D,B", [("bf16", 8, 128, 16), ("f16", 1, 64, 32), ("bf16", 3, 64, 16)])
