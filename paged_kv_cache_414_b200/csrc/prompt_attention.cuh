@@ -47,7 +47,8 @@ struct PromptParams {
   int max_query, max_key;
   int pieces;                  // pieces of the keys in the grid
   int piece_tiles;             // K/V tiles per piece
-  uint64_t wait_ns;
+  long long wait_cycles;       // limit of a wait before giving up
+  uint32_t wait_hint;          // and of one try, in ns
 };
 
 constexpr int kPrRows = 128;
@@ -76,9 +77,32 @@ struct PromptSmem {
   static constexpr int KV_BYTES = NCH * kPrKeys * 128;
   static constexpr int OFF_K = 2 * Q_TILE;
   static constexpr int OFF_V = OFF_K + STAGES * KV_BYTES;
-  static constexpr int OFF_BAR = OFF_V + STAGES * KV_BYTES;
-  static constexpr int BYTES = OFF_BAR + 1024;   // the slack aligns the base
+  static constexpr int BYTES = OFF_V + STAGES * KV_BYTES + 1024;   // the slack aligns the base
 };
+
+// Bounded wait that also gives up when another role has: a dozen instructions,
+// so that the kernel's loops stay within the instruction caches.  (With pf_wait
+// at every wait the kernel had 111 KB of code.)  The limit is in SM clock
+// cycles, two to a nanosecond; it is also the hint for how long one try may
+// sleep.  Who gives up sets `abort`, which the kernel reports at its end.
+__device__ __forceinline__ bool prompt_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                            long long limit_cycles, uint32_t hint_ns) {
+  if (mbar_test_wait(bar, parity)) return true;
+  const long long c0 = clock64();
+  uint32_t ok;
+  do {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(hint_ns)
+        : "memory");
+    if (ok) return true;
+  } while (!*abort && clock64() - c0 <= limit_cycles);
+  *abort = 1;
+  return false;
+}
 
 // ---------------------------------------------------------------- units
 
@@ -107,19 +131,28 @@ __device__ __forceinline__ bool prompt_find(const PromptParams &p, const int2 *c
   };
   auto at_least = [&](int e) {   // units of order e or more
     int n = 0;
+#pragma unroll 1
     for (int i = lane; i < p.num_seqs; i += 32) {
       const int2 q = seq(i);
       n += min(max(q.x + q.y - e, 0), q.y);
     }
     return __reduce_add_sync(0xffffffffu, n);
   };
-  if (v >= at_least(0)) return false;
-  int lo = 0, hi = (p.max_query + p.max_key) / (2 * p.tq) + 2;   // at_least(lo) > v >= at_least(hi)
+  // at_least(lo) > v >= at_least(hi) = above, once lo is known not to be -1
+  int lo = -1, hi = (p.max_query + p.max_key) / (2 * p.tq) + 2, above = 0;
+#pragma unroll 1
   while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (at_least(mid) > v) lo = mid; else hi = mid;
+    const int mid = (lo + hi) >> 1, n = at_least(mid);
+    if (n > v) {
+      lo = mid;
+    } else {
+      hi = mid;
+      above = n;
+    }
   }
-  int left = v - at_least(hi);
+  if (lo < 0) return false;
+  int left = v - above;
+#pragma unroll 1
   for (int i0 = 0; i0 < p.num_seqs; i0 += 32) {
     const int i = i0 + lane;
     const int2 q = i < p.num_seqs ? seq(i) : make_int2(0, 0);
@@ -187,6 +220,14 @@ __device__ __forceinline__ int cancelled_block(const void *answer) {
   return ok ? (int)x : -1;
 }
 
+// 32 bytes in one store (32-byte aligned).
+__device__ __forceinline__ void st_global_v8(void *dst, const uint32_t *v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                   reinterpret_cast<uint64_t>(dst)),
+               "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // max(a, b, c), NaN if any is.
 __device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
   float d;
@@ -210,7 +251,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 
   __shared__ uint64_t full_k[NST], full_v[NST], empty_k[NST], empty_v[NST];
   __shared__ uint64_t q_full, q_empty;      // both query tiles: landed, read by their last S
-  __shared__ uint64_t s_full[2], p_full[2], o_done[2];
+  __shared__ uint64_t s_full[2], p_half[2], p_full[2], o_done[2];
   __shared__ uint64_t v_tail, v_clean;      // the last V tile: landed; its tail is zeros
   __shared__ uint64_t unit_full[2], unit_empty[2];
   __shared__ uint64_t answer_bar, drain;
@@ -238,6 +279,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     mbar_init(&drain, 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&s_full[x], 1);
+      mbar_init(&p_half[x], 4);
       mbar_init(&p_full[x], 4);
       mbar_init(&o_done[x], 1);
       mbar_init(&unit_full[x], 1);
@@ -259,7 +301,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 
   // every lane waits; the warp goes on only if all of them saw the phase
   auto wait_all = [&](uint64_t *bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, pf_wait(bar, parity, abort, p.wait_ns));
+    return __all_sync(0xffffffffu, prompt_wait(bar, parity, abort, p.wait_cycles, p.wait_hint));
   };
   // the next unit, by its number in this CTA
   int taken = 0;
@@ -279,9 +321,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == 10) {
       // ------------------------------------------------------------ scheduler
+#pragma unroll 1
       for (int i = lane; i < min(p.num_seqs, kPrSeqCache); i += 32)
         seqs[i] = prompt_seq(p, i, blockIdx.x == 0);
       if (blockIdx.x == 0)
+#pragma unroll 1
         for (int i = kPrSeqCache + lane; i < p.num_seqs; i += 32) prompt_seq(p, i, true);
       __syncwarp();
       int block = blockIdx.x, made = 0, asked = 0;
@@ -406,14 +450,20 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           umma_ss_group4<0, 2, 4, 6>(d, dq, dk, idS, 0u);
         umma_commit(&s_full[x]);
       };
-      auto issue_pv = [&](int x, int st, bool first) {   // O_x (+)= P_x V
-        const uint64_t dv = dV0 + st * kStageStep;
-        const uint32_t pj = tmem + x * 256, d = pj + 128;
-        umma_ts_group8<0, 8, 16, 24, 32, 40, 48, 56, 0, 128, 256, 384, 512, 640, 768, 896>(
-            d, pj, dv, idO, first ? 0u : 1u);
+      // O_x (+)= P_x V, the first or last 64 keys of the tile
+      auto issue_pv0 = [&](int x, int st, bool first) {
+        const uint32_t pj = tmem + x * 256;
+        umma_ts_group4<0, 8, 16, 24, 0, 128, 256, 384>(pj + 128, pj, dV0 + st * kStageStep, idO,
+                                                       first ? 0u : 1u);
+      };
+      auto issue_pv1 = [&](int x, int st) {
+        const uint32_t pj = tmem + x * 256;
+        umma_ts_group4<32, 40, 48, 56, 512, 640, 768, 896>(pj + 128, pj, dV0 + st * kStageStep, idO,
+                                                           1u);
       };
       PromptUnit u;
-      int it = 0, nq = 0, np[2] = {0, 0}, nclean = 0;
+      unsigned it = 0, p_phase = 0;             // p_phase bit x: parity of the P awaited from tile x
+      int nq = 0, nclean = 0;
       bool ok = true;
       while (ok && next_unit(u)) {
         const int nm = max(u.n[0], u.n[1]);
@@ -423,8 +473,9 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         if (!ok) break;
         ++nq;
         tc_fence_after();
+#pragma unroll 1
         for (int x = 0; x < 2; ++x)
-          if (u.n[x] > 0) issue_s(x, it % NST);
+          if ((x ? u.n[1] : u.n[0]) > 0) issue_s(x, it % NST);
         umma_commit(&empty_k[it % NST]);
         if (nm == 1) umma_commit(&q_empty);
         for (int j = 0; ok && j < nm; ++j, ++it) {
@@ -437,14 +488,21 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           }
           if (ok && more) ok = wait_all(&full_k[sn], ((it + 1) / NST) & 1);
           if (!ok) break;
-#pragma unroll
+#pragma unroll 1
           for (int x = 0; x < 2; ++x) {
-            if (j >= u.n[x]) continue;
-            ok = wait_all(&p_full[x], np[x]++ & 1);
+            const int n = x ? u.n[1] : u.n[0];
+            if (j >= n) continue;
+            const uint32_t parity = (p_phase >> x) & 1;
+            p_phase ^= 1u << x;
+            ok = wait_all(&p_half[x], parity);
             if (!ok) break;
             tc_fence_after();
-            issue_pv(x, st, j == 0);
-            if (j + 1 == u.n[x]) umma_commit(&o_done[x]);
+            issue_pv0(x, st, j == 0);
+            ok = wait_all(&p_full[x], parity);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv1(x, st);
+            if (j + 1 == n) umma_commit(&o_done[x]);
             else issue_s(x, sn);
           }
           if (!ok) break;
@@ -482,15 +540,16 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int x = warp >> 2;                 // query tile
     const int r = threadIdx.x & 127;         // this thread's row, and lane of tensor memory
-    const int t = r / G, g = r - t * G;
+    const int t = r / G;
     const uint32_t tS = tmem + x * 256 + ((uint32_t)((warp & 3) * 32) << 16), tO = tS + 128;
+    const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
     const bool pos_scale = p.scale_log2 > 0.f;
     const float sl2 = pos_scale ? p.scale_log2 : 1.f;   // else the scores are scaled first
     PromptUnit u;
     int ns = 0, no = 0;
     bool ok = true;
     while (ok && next_unit(u)) {
-      const int n = u.n[x];
+      const int n = x ? u.n[1] : u.n[0];
       const bool row_ok = t < p.tq && x * p.tq + t < u.tokens;
       const int pos = row_ok ? u.pos0 + x * p.tq + t : u.pos0 + u.tokens - 1;
       const int pos_min = u.pos0 + x * p.tq;
@@ -499,21 +558,30 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         ok = wait_all(&s_full[x], ns & 1);
         if (!ok) break;
         tc_fence_after();
+        // keys past a row's position, and a scale that is not positive: the
+        // scores are first rewritten where they lie
+        const int lim = pos - j * kPrKeys;                     // keys 0 .. lim of the tile count
+        const bool masked = pos_min < j * kPrKeys + kPrKeys - 1;
+        if (masked || !pos_scale) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w[32];
+            tmem_load32(tS + c * 32, w);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float z = __uint_as_float(w[i]) * (pos_scale ? 1.f : p.scale_log2);
+              w[i] = c * 32 + i <= lim ? __float_as_uint(z) : 0xff800000u;   // -inf
+            }
+            tmem_store32_async(tS + c * 32, w);
+          }
+          tmem_store_wait();
+        }
         uint32_t v[128];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_load32_async(tS + c * 32, v + c * 32);
         tmem_load_wait();
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_loaded(v + c * 32);
-        const int lim = pos - j * kPrKeys;                     // keys 0 .. lim of the tile count
-        if (!pos_scale) {
-#pragma unroll
-          for (int i = 0; i < 128; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * p.scale_log2);
-        }
-        if (pos_min < j * kPrKeys + kPrKeys - 1) {
-#pragma unroll
-          for (int i = 0; i < 128; ++i) v[i] = i <= lim ? v[i] : 0xff800000u;   // -inf
-        }
         float mx[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(v[i]);
@@ -543,21 +611,28 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             tmem_store8(tO + c, o);
           }
         }
+        // weights, 32 keys at a time, and their sum
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t h[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int k = c * 32 + 2 * i;
-            float x0, x1;
+            const int k = c * 32 + 2 * i, s = (i & 1) * 2;
+            float x0, x1, p0, p1;
             ffma2(x0, x1, __uint_as_float(v[k]), __uint_as_float(v[k + 1]), sl2, sl2, -ref, -ref);
-            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-            fadd2(sum[(i & 1) * 2], sum[(i & 1) * 2 + 1], sum[(i & 1) * 2], sum[(i & 1) * 2 + 1], p0,
-                  p1);
+            p0 = fast_exp2(x0);
+            p1 = fast_exp2(x1);
+            fadd2(sum[s], sum[s + 1], sum[s], sum[s + 1], p0, p1);
             h[i] = Mma<T>::pack(p0, p1);
           }
           tmem_store16_async(tS + c * 16, h);
+          if (c == 1) {          // P.V may begin on the first half
+            tmem_store_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_half[x]);
+          }
         }
         l = l * alpha + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
         tmem_store_wait();
@@ -591,20 +666,26 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         const bool none = l == 0.f;          // nothing seen: zeros, whatever V holds
         const float inv = 1.f / l;
         T *dst = static_cast<T *>(p.out) +
-                 ((long long)(u.token0 + x * p.tq + t) * p.num_q_heads + u.kv_head * G + g) * D;
+                 ((long long)(u.token0 + x * p.tq + t) * p.num_q_heads + u.kv_head * G + r - t * G) * D;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          uint32_t o[16];
-          if (n > 0) tmem_load16(tO + c, o);
-          uint32_t h[8];
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32], h[16];
+          if (n > 0) tmem_load32(tO + c, o);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
+          for (int i = 0; i < 16; ++i)
             h[i] = none ? 0u
                         : Mma<T>::pack(__uint_as_float(o[2 * i]) * inv,
                                        __uint_as_float(o[2 * i + 1]) * inv);
           if (row_ok) {
-            *reinterpret_cast<uint4 *>(dst + c) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4 *>(dst + c + 8) = make_uint4(h[4], h[5], h[6], h[7]);
+            if (wide) {                      // whole 32-byte sectors
+              st_global_v8(dst + c, h);
+              st_global_v8(dst + c + 16, h + 8);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<uint4 *>(dst + c + 2 * i) =
+                    make_uint4(h[i], h[i + 1], h[i + 2], h[i + 3]);
+            }
           }
         }
       }
@@ -612,6 +693,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && abort_flag) flag_error(PA_DEVERR_TIMEOUT);
   if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, kPfTmemCols);
@@ -665,7 +747,7 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptParams p) 
       }
       M = mn;
     }
-    if (den == 0.f) {                 // nothing seen: zeros, whatever V holds
+    if (M == -INFINITY) {             // nothing seen: zeros, whatever V holds
 #pragma unroll
       for (int i = 0; i < VPL; ++i) num[i] = 0.f;
       den = 1.f;

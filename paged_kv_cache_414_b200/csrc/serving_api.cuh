@@ -532,7 +532,9 @@ int pa_prompt_attention(void *out, const void *q, const void *key, const void *v
   p.max_key = max_key_len;
   p.pieces = pl.pieces;
   p.piece_tiles = pl.piece_tiles;
-  p.wait_ns = g_wait_limit_ns.load();
+  const unsigned long long limit = std::min(g_wait_limit_ns.load(), 1ull << 60);
+  p.wait_cycles = 2 * (long long)limit;
+  p.wait_hint = (uint32_t)std::min(limit, 1000000ull);
   cudaStream_t st = (cudaStream_t)stream;
   if (dtype == PA_BF16)
     return head_dim == 128
