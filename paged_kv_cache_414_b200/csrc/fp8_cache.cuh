@@ -32,11 +32,10 @@ struct RopeParams {
   const float *cos_sin;        // [max_position, rotary]: cosines, then sines
   long long q_out_stride, q_stride, k_stride, v_stride;
   long long num_slots;
-  long long units;             // T * head_slots
   int num_tokens, num_q_heads, num_kv_heads, block_size;
   int rotary, axes, max_position;
   int sect[3];                 // frequency pairs before axis 1, 2, 3
-  int head_slots;              // ceil((Hq + 2 Hkv) / heads per thread)
+  int splits, passes;          // warps to a token, and passes of each
 };
 
 // Rotary positions and the cache write.  Frequency pair j of a head's first
@@ -45,72 +44,81 @@ struct RopeParams {
 // (a, b) = columns (j, j + rotary/2), or (2j, 2j + 1) with PAIRS.  D/16 lanes
 // share a head row, 16 columns each, chosen so that lane l owns the pairs
 // 8l .. 8l+7 in either order and both its loads and its 16-bit stores are
-// 16-byte vectors; a row's amax is a shuffle among its lanes.  A thread takes
-// HPT heads of one token, `head_slots` apart, so that neighbouring lanes read
-// neighbouring rows and the table's cosines and sines are fetched once for all
-// of them; all its rows are loaded before any is stored.
-template <typename T, int D, bool FP8, bool PAIRS, int HPT>
-__global__ void __launch_bounds__(256) rope_and_cache_kernel(const RopeParams p) {
-  constexpr int LPR = D / 16;
+// 16-byte vectors; a row's amax is a shuffle among its lanes.
+//
+// A warp takes a token's heads 512 / D at a time, so that the cosines and sines
+// of its lanes are fetched once per token; a pass's rows are loaded two passes
+// ahead, the next token's positions and slot a token ahead.  With few tokens `splits` warps share one.  Bound: HBM; 16384
+// tokens of 32 q and 8 kv heads took 119 us with four heads to a thread and no
+// loop (15 warps per SM, all waiting for the same things at the same time).
+template <typename T, int D, bool FP8, bool PAIRS>
+__global__ void __launch_bounds__(256, 3) rope_and_cache_kernel(const RopeParams p) {
+  constexpr int LPR = D / 16, HPP = 32 / LPR;   // lanes of a head row, heads of a pass
   grid_dependency_wait();
   allow_dependent_launch();
-  const int l = threadIdx.x % LPR;
-  const long long u = (long long)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
-  // lanes past the last unit repeat it without storing: the shuffles below
-  // need whole warps
-  const bool live = u < p.units;
-  const long long uu = live ? u : p.units - 1;
-  const long long t = uu / p.head_slots;
-  const int hs = (int)(uu - t * p.head_slots);
+  const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
   const int nq = p.num_q_heads, nk = nq + p.num_kv_heads, nv = nk + p.num_kv_heads;
+  const int units = p.num_tokens * p.splits, step = gridDim.x * 8;
+  int unit = blockIdx.x * 8 + (threadIdx.x >> 5);
 
-  // the token's positions, one per axis; a bad one skips the token
-  bool ok = live;
-  long long pos[4];
-#pragma unroll
-  for (int a = 0; a < 4; ++a) {
-    pos[a] = a < p.axes ? p.positions[(long long)a * p.num_tokens + t] : 0;
-    if (a < p.axes && (pos[a] < 0 || pos[a] >= p.max_position)) {
-      if (live && hs == 0 && l == 0) flag_error(PA_DEVERR_POSITION);
-      ok = false;
-      pos[a] = 0;
-    }
-  }
   const bool turns = 16 * l < p.rotary;
   const int e0 = PAIRS || !turns ? 16 * l : 8 * l;
   const int e1 = PAIRS || !turns ? 16 * l + 8 : p.rotary / 2 + 8 * l;
+  const int j0 = 8 * l;
+  auto axis_of = [&](int j) {
+    return (j >= p.sect[0] ? 1 : 0) + (j >= p.sect[1] ? 1 : 0) + (j >= p.sect[2] ? 1 : 0);
+  };
+  const int axis0 = axis_of(j0);
+  const bool one_axis = axis0 == axis_of(j0 + 7);
+  const bool mixed = __any_sync(0xffffffffu, turns && !one_axis);
 
-  // this lane's 16 columns of each of its heads
-  uint4 x[HPT][2];
-#pragma unroll
-  for (int i = 0; i < HPT; ++i) {
-    const int h = hs + i * p.head_slots;
-    const T *row = nullptr;
-    if (ok && h < nq) {
-      if (p.q) row = static_cast<const T *>(p.q) + t * p.q_stride + (long long)h * D;
-    } else if (ok && h < nk) {
-      row = static_cast<const T *>(p.k) + t * p.k_stride + (long long)(h - nq) * D;
-    } else if (ok && h < nv) {
-      row = static_cast<const T *>(p.v) + t * p.v_stride + (long long)(h - nk) * D;
+  // lane a < axes: the token's position on that axis; lane 4: its slot
+  auto fetch = [&](int u) -> long long {
+    if (u >= units) return 0;
+    const int t = u / p.splits;
+    if (lane < p.axes) return p.positions[(long long)lane * p.num_tokens + t];
+    return lane == 4 ? p.slots[t] : 0;
+  };
+  long long next = fetch(unit);
+  for (; unit < units; unit += step) {
+    const long long now = next;
+    next = fetch(unit + step);
+    const int t = unit / p.splits, part = unit - t * p.splits;
+    const bool bad = lane < p.axes && (now < 0 || now >= p.max_position);
+    const long long slot = __shfl_sync(0xffffffffu, now, 4);
+    if (__any_sync(0xffffffffu, bad)) {   // the token is skipped altogether
+      if (bad && part == 0) flag_error(PA_DEVERR_POSITION);
+      continue;
     }
-    x[i][0] = row ? *reinterpret_cast<const uint4 *>(row + e0) : make_uint4(0, 0, 0, 0);
-    x[i][1] = row ? *reinterpret_cast<const uint4 *>(row + e1) : make_uint4(0, 0, 0, 0);
-  }
-  const int64_t slot = p.slots ? p.slots[t] : -1;
+    bool keep = slot >= 0;
+    if (slot >= p.num_slots) {
+      if (part == 0 && lane == 0) flag_error(PA_DEVERR_SLOT);
+      keep = false;
+    }
+    const long long blk = keep ? slot / p.block_size : 0;
+    const int off = keep ? (int)(slot - blk * p.block_size) : 0;
+    const int first = part * p.passes * HPP + sub;          // this lane's first head
 
-  float c[8], s[8];
-  if (turns && hs < nk) {
-    const int j0 = 8 * l;
-    auto axis = [&](int j) {
-      return (j >= p.sect[0] ? 1 : 0) + (j >= p.sect[1] ? 1 : 0) + (j >= p.sect[2] ? 1 : 0);
+    uint4 x0[2], x1[2];                                     // the next two passes' rows
+    auto load = [&](int h, uint4 (&y)[2]) {
+      const T *row = nullptr;
+      if (h < nq)
+        row = static_cast<const T *>(p.q) + t * p.q_stride + (long long)h * D;
+      else if (h < nk)
+        row = static_cast<const T *>(p.k) + t * p.k_stride + (long long)(h - nq) * D;
+      else if (h < nv)
+        row = static_cast<const T *>(p.v) + t * p.v_stride + (long long)(h - nk) * D;
+      y[0] = row ? *reinterpret_cast<const uint4 *>(row + e0) : make_uint4(0, 0, 0, 0);
+      y[1] = row ? *reinterpret_cast<const uint4 *>(row + e1) : make_uint4(0, 0, 0, 0);
     };
-    auto line = [&](int j) {
-      const int a = axis(j);
-      const long long ps = a == 0 ? pos[0] : (a == 1 ? pos[1] : (a == 2 ? pos[2] : pos[3]));
-      return p.cos_sin + ps * p.rotary + j;
-    };
-    if (axis(j0) == axis(j0 + 7)) {
-      const float *f = line(j0);
+    const int passes = min(p.passes, (nv - part * p.passes * HPP + HPP - 1) / HPP);
+    load(first, x0);
+    load(passes > 1 ? first + HPP : nv, x1);                // (nv: no row)
+
+    float c[8], s[8];
+    const long long pos = __shfl_sync(0xffffffffu, now, axis0);
+    if (turns && one_axis) {
+      const float *f = p.cos_sin + pos * p.rotary + j0;
 #pragma unroll
       for (int m = 0; m < 8; m += 4) {
         const float4 fc = __ldg(reinterpret_cast<const float4 *>(f + m));
@@ -118,96 +126,91 @@ __global__ void __launch_bounds__(256) rope_and_cache_kernel(const RopeParams p)
         c[m] = fc.x, c[m + 1] = fc.y, c[m + 2] = fc.z, c[m + 3] = fc.w;
         s[m] = fs.x, s[m + 1] = fs.y, s[m + 2] = fs.z, s[m + 3] = fs.w;
       }
-    } else {   // a section ends among these pairs
+    }
+    if (mixed) {                          // a section ends among some lane's pairs
 #pragma unroll
       for (int m = 0; m < 8; ++m) {
-        const float *f = line(j0 + m);
-        c[m] = __ldg(f);
-        s[m] = __ldg(f + p.rotary / 2);
+        const long long at = __shfl_sync(0xffffffffu, now, axis_of(j0 + m));
+        if (turns && !one_axis) {
+          const float *f = p.cos_sin + at * p.rotary + j0 + m;
+          c[m] = __ldg(f);
+          s[m] = __ldg(f + p.rotary / 2);
+        }
       }
     }
-  } else {
-#pragma unroll
-    for (int m = 0; m < 8; ++m) c[m] = 1.f, s[m] = 0.f;
-  }
 
-  bool keep = ok && slot >= 0;
-  if (slot >= p.num_slots) {
-    if (ok && hs == 0 && l == 0) flag_error(PA_DEVERR_SLOT);
-    keep = false;
-  }
-  const long long blk = keep ? slot / p.block_size : 0;
-  const int off = keep ? (int)(slot - blk * p.block_size) : 0;
-
+    auto finish = [&](int h, const uint4 (&y)[2]) {
+      const bool is_q = h < nq, is_k = !is_q && h < nk, is_v = !is_q && !is_k && h < nv;
+      float f[16];   // columns e0 .. e0+7, then e1 .. e1+7
 #pragma unroll
-  for (int i = 0; i < HPT; ++i) {
-    const int h = hs + i * p.head_slots;
-    const bool is_q = h < nq, is_k = !is_q && h < nk, is_v = !is_q && !is_k && h < nv;
-    float f[16];   // columns e0 .. e0+7, then e1 .. e1+7
+      for (int w = 0; w < 2; ++w) {
+        const uint32_t g[4] = {y[w].x, y[w].y, y[w].z, y[w].w};
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const uint32_t g[4] = {x[i][w].x, x[i][w].y, x[i][w].z, x[i][w].w};
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const float2 v2 = Mma<T>::unpack(g[m]);
-        f[8 * w + 2 * m] = v2.x;
-        f[8 * w + 2 * m + 1] = v2.y;
+        for (int m = 0; m < 4; ++m) {
+          const float2 v2 = Mma<T>::unpack(g[m]);
+          f[8 * w + 2 * m] = v2.x;
+          f[8 * w + 2 * m + 1] = v2.y;
+        }
       }
-    }
-    if (!is_v && turns) {
+      if (!is_v && turns) {
 #pragma unroll
-      for (int m = 0; m < 8; ++m) {
-        const int ia = PAIRS ? 2 * m : m, ib = PAIRS ? 2 * m + 1 : m + 8;
-        const float a = f[ia], b = f[ib];
-        f[ia] = a * c[m] - b * s[m];
-        f[ib] = b * c[m] + a * s[m];
+        for (int m = 0; m < 8; ++m) {
+          const int ia = PAIRS ? 2 * m : m, ib = PAIRS ? 2 * m + 1 : m + 8;
+          const float a = f[ia], b = f[ib];
+          f[ia] = a * c[m] - b * s[m];
+          f[ib] = b * c[m] + a * s[m];
+        }
       }
-    }
-    float amax = 0.f;
-    if (FP8) {
+      if (FP8 && __any_sync(0xffffffffu, h >= nq)) {   // some K or V row in this pass
+        float amax = 0.f;
 #pragma unroll
-      for (int m = 0; m < 16; ++m) amax = fmaxf(amax, fabsf(f[m]));
+        for (int m = 0; m < 16; ++m) amax = fmaxf(amax, fabsf(f[m]));
 #pragma unroll
-      for (int d = 1; d < LPR; d <<= 1)
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-    }
-    if (is_q || !FP8) {
-      uint4 y[2];
+        for (int d = 1; d < LPR; d <<= 1)
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+        if (keep && (is_k || is_v)) {
+          const float top = fmaxf(amax, kLeastAmax);
+          const float inv = kE4m3Max / top;
+          uint32_t w4[4];
 #pragma unroll
-      for (int w = 0; w < 2; ++w)
-        y[w] = make_uint4(Mma<T>::pack(f[8 * w], f[8 * w + 1]),
-                          Mma<T>::pack(f[8 * w + 2], f[8 * w + 3]),
-                          Mma<T>::pack(f[8 * w + 4], f[8 * w + 5]),
-                          Mma<T>::pack(f[8 * w + 6], f[8 * w + 7]));
+          for (int m = 0; m < 4; ++m) {
+            const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(
+                make_float2(f[4 * m] * inv, f[4 * m + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+            const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(
+                make_float2(f[4 * m + 2] * inv, f[4 * m + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+            w4[m] = (uint32_t)lo | ((uint32_t)hi << 16);
+          }
+          const long long tile = blk * p.num_kv_heads + (is_k ? h - nq : h - nk);
+          uint8_t *row = static_cast<uint8_t *>(is_k ? p.k_cache : p.v_cache) +
+                         (tile * p.block_size + off) * D;
+          *reinterpret_cast<uint2 *>(row + e0) = make_uint2(w4[0], w4[1]);
+          *reinterpret_cast<uint2 *>(row + e1) = make_uint2(w4[2], w4[3]);
+          if (l == 0)
+            p.kv_scale[(tile * 2 + (is_k ? 0 : 1)) * p.block_size + off] = top / kE4m3Max;
+        }
+      }
       T *row = nullptr;
-      if (is_q) {
-        if (ok && p.q) row = static_cast<T *>(p.q_out) + t * p.q_out_stride + (long long)h * D;
-      } else if (keep && (is_k || is_v)) {
+      if (is_q)
+        row = static_cast<T *>(p.q_out) + t * p.q_out_stride + (long long)h * D;
+      else if (!FP8 && keep && (is_k || is_v))
         row = static_cast<T *>(is_k ? p.k_cache : p.v_cache) +
               ((blk * p.num_kv_heads + (is_k ? h - nq : h - nk)) * p.block_size + off) * D;
-      }
       if (row) {
-        *reinterpret_cast<uint4 *>(row + e0) = y[0];
-        *reinterpret_cast<uint4 *>(row + e1) = y[1];
-      }
-    } else if (keep && (is_k || is_v)) {
-      const float top = fmaxf(amax, kLeastAmax);
-      const float inv = kE4m3Max / top;
-      uint32_t w4[4];
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(
-            make_float2(f[4 * m] * inv, f[4 * m + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-        const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(
-            make_float2(f[4 * m + 2] * inv, f[4 * m + 3] * inv), __NV_SATFINITE, __NV_E4M3);
-        w4[m] = (uint32_t)lo | ((uint32_t)hi << 16);
+        for (int w = 0; w < 2; ++w)
+          *reinterpret_cast<uint4 *>(row + (w ? e1 : e0)) =
+              make_uint4(Mma<T>::pack(f[8 * w], f[8 * w + 1]),
+                         Mma<T>::pack(f[8 * w + 2], f[8 * w + 3]),
+                         Mma<T>::pack(f[8 * w + 4], f[8 * w + 5]),
+                         Mma<T>::pack(f[8 * w + 6], f[8 * w + 7]));
       }
-      const long long tile = blk * p.num_kv_heads + (is_k ? h - nq : h - nk);
-      uint8_t *row = static_cast<uint8_t *>(is_k ? p.k_cache : p.v_cache) +
-                     (tile * p.block_size + off) * D;
-      *reinterpret_cast<uint2 *>(row + e0) = make_uint2(w4[0], w4[1]);
-      *reinterpret_cast<uint2 *>(row + e1) = make_uint2(w4[2], w4[3]);
-      if (l == 0) p.kv_scale[(tile * 2 + (is_k ? 0 : 1)) * p.block_size + off] = top / kE4m3Max;
+    };
+#pragma unroll 1
+    for (int i = 0; i < passes; ++i) {
+      const uint4 y[2] = {x0[0], x0[1]};
+      x0[0] = x1[0], x0[1] = x1[1];
+      load(i + 2 < passes ? first + (i + 2) * HPP : nv, x1);
+      finish(first + i * HPP, y);
     }
   }
 }

@@ -35,32 +35,28 @@ cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, int threads, siz
 // ---------------------------------------------------------------- rotary cache write
 
 template <typename T, int D, bool FP8, bool PAIRS>
-int launch_rope(pa::RopeParams &p, cudaStream_t stream) {
-  constexpr int LPR = D / 16;
-  const int heads = p.num_q_heads + 2 * p.num_kv_heads;
-  // One head per thread while the call is too small to fill the GPU, four
-  // (which share the table's row) once it is not.
-  const bool many = (long long)p.num_tokens * heads * LPR >= 148ll * 2048 * 4;
-  const int hpt = many ? 4 : 1;
-  p.head_slots = (heads + hpt - 1) / hpt;
-  p.units = (long long)p.num_tokens * p.head_slots;
-  const long long blocks = (p.units + 256 / LPR - 1) / (256 / LPR);
-  if (blocks >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
-  const cudaError_t e =
-      many ? launch_dependent(pa::rope_and_cache_kernel<T, D, FP8, PAIRS, 4>, dim3((unsigned)blocks),
-                              256, 0, stream, p)
-           : launch_dependent(pa::rope_and_cache_kernel<T, D, FP8, PAIRS, 1>, dim3((unsigned)blocks),
-                              256, 0, stream, p);
+int launch_rope(pa::RopeParams &p, int sms, cudaStream_t stream) {
+  constexpr int HPP = 512 / D;   // heads of a pass
+  const int heads = p.num_q_heads + 2 * p.num_kv_heads, all = (heads + HPP - 1) / HPP;
+  // As many warps to a token as leave every SM its 24, one pass each at most.
+  const long long resident = 24ll * sms;
+  p.splits = (int)std::max(1ll, std::min<long long>(all, resident / p.num_tokens));
+  p.passes = (all + p.splits - 1) / p.splits;
+  p.splits = (all + p.passes - 1) / p.passes;
+  const long long units = (long long)p.num_tokens * p.splits;
+  const unsigned grid = (unsigned)std::min<long long>((units + 7) / 8, 3ll * sms);
+  const cudaError_t e = launch_dependent(pa::rope_and_cache_kernel<T, D, FP8, PAIRS>, dim3(grid),
+                                         256, 0, stream, p);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 template <typename T, int D>
-int dispatch_rope(pa::RopeParams &p, bool fp8, bool pairs, cudaStream_t stream) {
+int dispatch_rope(pa::RopeParams &p, bool fp8, bool pairs, int sms, cudaStream_t stream) {
   if (fp8)
-    return pairs ? launch_rope<T, D, true, true>(p, stream)
-                 : launch_rope<T, D, true, false>(p, stream);
-  return pairs ? launch_rope<T, D, false, true>(p, stream)
-               : launch_rope<T, D, false, false>(p, stream);
+    return pairs ? launch_rope<T, D, true, true>(p, sms, stream)
+                 : launch_rope<T, D, true, false>(p, sms, stream);
+  return pairs ? launch_rope<T, D, false, true>(p, sms, stream)
+               : launch_rope<T, D, false, false>(p, sms, stream);
 }
 
 int rope_and_cache(bool fp8, void *q_out, const void *q, const void *key, const void *value,
@@ -103,6 +99,12 @@ int rope_and_cache(bool fp8, void *q_out, const void *q, const void *key, const 
       (q && (!aligned_stride(q_stride, head_dim, num_q_heads) ||
              !aligned_stride(q_out_stride, head_dim, num_q_heads))))
     return PA_ERR_ARG;
+  if (num_tokens >= (1 << 30) || num_kv_heads > (1 << 20) || num_q_heads > (1 << 20))
+    return PA_ERR_UNSUPPORTED;
+  int dev;
+  if (current_device(&dev) != PA_OK) return PA_ERR_CUDA;
+  const int sms = sm_count(dev);
+  if (sms <= 0) return PA_ERR_CUDA;
   pa::RopeParams p;
   p.q_out = q_out;
   p.q = q;
@@ -128,10 +130,10 @@ int rope_and_cache(bool fp8, void *q_out, const void *q, const void *key, const 
   p.max_position = max_position;
   for (int a = 0; a < 3; ++a) p.sect[a] = bound[a];
   if (dtype == PA_BF16)
-    return head_dim == 128 ? dispatch_rope<__nv_bfloat16, 128>(p, fp8, interleaved != 0, stream)
-                           : dispatch_rope<__nv_bfloat16, 64>(p, fp8, interleaved != 0, stream);
-  return head_dim == 128 ? dispatch_rope<__half, 128>(p, fp8, interleaved != 0, stream)
-                         : dispatch_rope<__half, 64>(p, fp8, interleaved != 0, stream);
+    return head_dim == 128 ? dispatch_rope<__nv_bfloat16, 128>(p, fp8, interleaved != 0, sms, stream)
+                           : dispatch_rope<__nv_bfloat16, 64>(p, fp8, interleaved != 0, sms, stream);
+  return head_dim == 128 ? dispatch_rope<__half, 128>(p, fp8, interleaved != 0, sms, stream)
+                         : dispatch_rope<__half, 64>(p, fp8, interleaved != 0, sms, stream);
 }
 
 // ---------------------------------------------------------------- 8-bit decode
