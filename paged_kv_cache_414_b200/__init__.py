@@ -1,7 +1,7 @@
 """Python binding of libpa.so, the B200 paged-KV-cache attention library.
 
-Argument marshalling only: every function here checks the torch tensors it is
-given, passes their device pointers, sizes and the current CUDA stream to the
+Argument marshalling only: every function here (the shortest calls through the
+extension module _calls) checks the torch tensors it is given, passes their device pointers, sizes and the current CUDA stream to the
 C ABI declared in include/pa.h, and raises on a non-zero status.  No step of
 the computation runs in Python, and there is no fallback: if libpa.so is
 missing or a call fails, an exception is raised.
@@ -18,7 +18,6 @@ caching included).
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 import numpy as np
@@ -352,124 +351,37 @@ def pa_device_error(clear: bool = True) -> int:
 
 # ------------------------------------------------- rotary positions, 8-bit pool, prompts
 #
-# A small call takes a few microseconds on the GPU, so each tensor is looked at
-# once, in one expression, and only a call that is about to raise asks why.
+# These calls take a few microseconds on the GPU, so their arguments are checked
+# and passed on in the extension module _calls.
 
-def _place(t, name):
-    """The current CUDA device, where the call launches; the tensor must lie there."""
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    here = _torch()._C._cuda_getDevice()
-    if dev != here:
-        raise ValueError(f"{name} is on cuda:{dev}, the current device is {here}")
-    return dev
+_calls_module = None
 
 
-def _refuse(t, name, dtype, shape, dev):
-    if t.get_device() < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is {dev}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    raise ValueError(f"{name} must be contiguous")
+def _bind(L):
+    """Hand the library's entry points to the extension module."""
+    global _calls_module
+    try:
+        from . import _calls
+    except ImportError as e:
+        raise ImportError("the extension module _calls is missing: build it with "
+                          "`python -m paged_kv_cache_414_b200.build`") from e
+    _calls.bind(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
+        "pa_rope_and_cache", "pa_rope_and_cache_fp8", "pa_paged_decode_workspace_bytes",
+        "pa_paged_decode_attention_fp8", "pa_copy_blocks_fp8", "pa_gather_cache_fp8",
+        "pa_prompt_attention_workspace_bytes", "pa_prompt_attention")))
+    _calls_module = _calls
+    return _calls
 
 
-def _flat(t, name, dtype, shape, dev):
-    """Pointer of a dense tensor of that dtype and shape on the device."""
-    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
-    _refuse(t, name, dtype, shape, dev)
+def _native():
+    if _calls_module is not None:
+        return _calls_module
+    _torch()     # the module needs torch's libraries
+    return _bind(lib())
 
 
-def _rows(t, name, dtype, shape, dev):
-    """(pointer, row stride in elements) of [tokens, heads, head_dim] whose tokens may lie
-    apart (columns of a fused projection) and whose heads are dense."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
-        _refuse(t, name, dtype, shape, dev)
-    n, h, d = shape
-    s0, s1, s2 = t.stride()
-    if n <= 1:
-        s0 = h * d
-    if n > 0 and (s2 != 1 or (h > 1 and s1 != d)):
-        raise ValueError(f"{name}: the heads of a token must be dense")
-    if s0 < h * d or s0 % 8:
-        raise ValueError(f"{name}: token stride {s0} must be a multiple of 8, at least {h * d}")
-    return t.data_ptr(), s0
-
-
-def _bytes(workspace, dev):
-    if workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the current CUDA device")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
-
-def _scratch(nbytes, like, stream):
-    """Workspace of one call, on the stream that uses it."""
-    w = _torch().empty(nbytes, dtype=_torch().uint8, device=like.device)
-    if stream is not None:   # allocated on the current stream, used on another
-        w.record_stream(stream)
-    return w
-
-
-def _on(stream, dev):
-    if stream is None:
-        return _torch()._C._cuda_getCurrentRawStream(dev)
-    return stream.cuda_stream
-
-
-def _pool_fp8(k_cache, v_cache, kv_scale, dev):
-    torch = _torch()
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache must be [num_blocks, num_kv_heads, block_size, head_dim]")
-    shape = k_cache.shape
-    NB, Hkv, B, _ = shape
-    return (_flat(k_cache, "k_cache", torch.float8_e4m3fn, shape, dev),
-            _flat(v_cache, "v_cache", torch.float8_e4m3fn, shape, dev),
-            _flat(kv_scale, "kv_scale", torch.float32, (NB, Hkv, 2, B), dev))
-
-
-@functools.lru_cache(maxsize=64)
-def _sections(sections):
-    return (ctypes.c_int * len(sections))(*sections)
-
-
-def _rope(name, q_out, q, key, value, pool, shape, slot_mapping, positions, cos_sin, sections,
-          interleaved, stream, dev):
-    torch = _torch()
-    NB, Hkv, B, D = shape
-    T = key.shape[0]
-    dt = key.dtype
-    code = _dtype_code(key)
-    k, ks = _rows(key, "key", dt, (T, Hkv, D), dev)
-    v, vs = _rows(value, "value", dt, (T, Hkv, D), dev)
-    slots = _flat(slot_mapping, "slot_mapping", torch.int64, (T,), dev)
-    Hq = qs = qos = rot = axes = most = 0
-    qp = qo = pos = table = sect = None
-    if q is not None:
-        Hq = q.shape[1] if q.dim() == 3 else 0
-        qp, qs = _rows(q, "q", dt, (T, Hq, D), dev)
-        qo, qos = _rows(q_out, "q_out", dt, (T, Hq, D), dev)
-    if cos_sin is not None:
-        if cos_sin.dim() != 2:
-            raise ValueError("cos_sin must be [max_position, rotary_dim]")
-        most, rot = cos_sin.shape
-        table = _flat(cos_sin, "cos_sin", torch.float32, (most, rot), dev)
-        axes = positions.shape[0] if positions.dim() == 2 else 1
-        pos = _flat(positions, "positions", torch.int64,
-                    (axes, T) if positions.dim() == 2 else (T,), dev)
-        sections = (rot // 2,) if sections is None else tuple(sections)
-        if len(sections) != axes:
-            raise ValueError(f"sections must name every axis: {axes} of them, got {len(sections)}")
-        sect = _sections(sections)
-    st = getattr(lib(), name)(qo, qp, k, v, *pool, slots, pos, table, sect, axes, rot, most,
-                              interleaved, qos, qs, ks, vs, T, Hq, Hkv, D, B, NB, code,
-                              _on(stream, dev))
-    if st:
-        _check(st, name)
+def _raw(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def pa_rope_and_cache(q_out, q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin,
@@ -483,24 +395,22 @@ def pa_rope_and_cache(q_out, q, key, value, k_cache, v_cache, slot_mapping, posi
     sections: frequency pairs of each axis, e.g. (16, 24, 24) for time, height and width (default:
     one axis); interleaved: pairs are columns (2j, 2j+1) instead of (j, j + rotary_dim/2).
     cos_sin None stores without turning."""
-    dev = _place(key, "key")
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache must be [num_blocks, num_kv_heads, block_size, head_dim]")
-    shape = k_cache.shape
-    pool = (_flat(k_cache, "k_cache", key.dtype, shape, dev),
-            _flat(v_cache, "v_cache", key.dtype, shape, dev))
-    _rope("pa_rope_and_cache", q_out, q, key, value, pool, shape, slot_mapping, positions,
-          cos_sin, sections, interleaved, stream, dev)
+    st = _native().rope(q_out, q, key, value, k_cache, v_cache, None, slot_mapping, positions,
+                         cos_sin, sections, interleaved, _raw(stream))
+    if st:
+        _check(st, "pa_rope_and_cache")
 
 
 def pa_rope_and_cache_fp8(q_out, q, key, value, k_cache, v_cache, kv_scale, slot_mapping,
                           positions, cos_sin, sections=None, interleaved=False, stream=None):
     """pa_rope_and_cache into the 8-bit pool: k_cache, v_cache float8_e4m3fn [num_blocks, Hkv, B, D]
     and kv_scale fp32 [num_blocks, Hkv, 2, B], one scale per token's K row and V row."""
-    dev = _place(key, "key")
-    _rope("pa_rope_and_cache_fp8", q_out, q, key, value,
-          _pool_fp8(k_cache, v_cache, kv_scale, dev), k_cache.shape, slot_mapping, positions,
-          cos_sin, sections, interleaved, stream, dev)
+    if kv_scale is None:
+        raise TypeError("kv_scale must be a torch tensor")
+    st = _native().rope(q_out, q, key, value, k_cache, v_cache, kv_scale, slot_mapping, positions,
+                         cos_sin, sections, interleaved, _raw(stream))
+    if st:
+        _check(st, "pa_rope_and_cache_fp8")
 
 
 def pa_paged_decode_attention_fp8(out, q, k_cache, v_cache, kv_scale, block_tables, context_lens,
@@ -508,27 +418,8 @@ def pa_paged_decode_attention_fp8(out, q, k_cache, v_cache, kv_scale, block_tabl
                                   stream=None):
     """pa_paged_decode_attention over the 8-bit pool: out[s, h] = softmax(scale * q[s, h] K_s^T) V_s
     with K and V the cached codes times their scales; q 16 bits, out fp32."""
-    torch = _torch()
-    dev = _place(q, "q")
-    pool = _pool_fp8(k_cache, v_cache, kv_scale, dev)
-    NB, Hkv, B, D = k_cache.shape
-    if q.dim() != 3 or Hkv != num_kv_heads or block_tables.dim() != 2:
-        raise ValueError("q [S, Hq, D], block_tables [S, max_blocks] and a cache of num_kv_heads "
-                         "heads expected")
-    S, Hq, _ = q.shape
-    maxb = block_tables.shape[1]
-    code = _dtype_code(q)
-    if max_context_len is None:
-        max_context_len = maxb * B
-    if workspace is None:
-        workspace = _scratch(pa_paged_decode_workspace_bytes(S, Hq, Hkv, D, B, max_context_len),
-                             q, stream)
-    wp, wb = _bytes(workspace, dev)
-    st = lib().pa_paged_decode_attention_fp8(
-        _flat(out, "out", torch.float32, (S, Hq, D), dev), _flat(q, "q", q.dtype, (S, Hq, D), dev),
-        *pool, _flat(block_tables, "block_tables", torch.int32, (S, maxb), dev),
-        _flat(context_lens, "context_lens", torch.int32, (S,), dev), scale, Hkv, S, Hq, D, B, maxb,
-        max_context_len, NB, code, wp, wb, _on(stream, dev))
+    st = _native().decode_fp8(out, q, k_cache, v_cache, kv_scale, block_tables, context_lens, scale,
+                               num_kv_heads, max_context_len, workspace, _raw(stream))
     if st:
         _check(st, "pa_paged_decode_attention_fp8")
     return out
@@ -536,12 +427,7 @@ def pa_paged_decode_attention_fp8(out, q, k_cache, v_cache, kv_scale, block_tabl
 
 def pa_copy_blocks_fp8(k_cache, v_cache, kv_scale, block_mapping, stream=None):
     """pa_copy_blocks on the 8-bit pool: codes and scales of every (src, dst) row."""
-    dev = _place(k_cache, "k_cache")
-    pool = _pool_fp8(k_cache, v_cache, kv_scale, dev)
-    NB, Hkv, B, D = k_cache.shape
-    n = block_mapping.shape[0] if block_mapping.dim() == 2 else 0
-    pairs = _flat(block_mapping, "block_mapping", _torch().int64, (n, 2), dev)
-    st = lib().pa_copy_blocks_fp8(*pool, pairs, n, Hkv, D, B, NB, _on(stream, dev))
+    st = _native().copy_fp8(k_cache, v_cache, kv_scale, block_mapping, _raw(stream))
     if st:
         _check(st, "pa_copy_blocks_fp8")
 
@@ -550,21 +436,8 @@ def pa_gather_cache_fp8(key, value, k_cache, v_cache, kv_scale, block_tables, ke
                         stream=None):
     """Cached rows out of the 8-bit pool: rows key_start[s] .. key_start[s+1]-1 of key and value
     [T, Hkv, D] (16 bits) become positions 0, 1, ... of sequence s; later rows are left."""
-    torch = _torch()
-    dev = _place(key, "key")
-    pool = _pool_fp8(k_cache, v_cache, kv_scale, dev)
-    NB, Hkv, B, D = k_cache.shape
-    if key_start.dim() != 1 or block_tables.dim() != 2:
-        raise ValueError("block_tables [S, max_blocks] and key_start [S + 1] expected")
-    S = max(0, key_start.shape[0] - 1)
-    maxb = block_tables.shape[1]
-    T = key.shape[0]
-    st = lib().pa_gather_cache_fp8(
-        _flat(key, "key", key.dtype, (T, Hkv, D), dev),
-        _flat(value, "value", key.dtype, (T, Hkv, D), dev), *pool,
-        _flat(block_tables, "block_tables", torch.int32, (S, maxb), dev),
-        _flat(key_start, "key_start", torch.int32, (S + 1,), dev), S, T, Hkv, D, B, maxb, NB,
-        _dtype_code(key), _on(stream, dev))
+    st = _native().gather_fp8(key, value, k_cache, v_cache, kv_scale, block_tables, key_start,
+                               _raw(stream))
     if st:
         _check(st, "pa_gather_cache_fp8")
 
@@ -576,29 +449,8 @@ def pa_prompt_attention(out, q, key, value, query_start, key_start, scale, num_k
     [T, Hq, D] and key_start[s] .. of key and value [Tk, Hkv, D] (16 bits, tokens any multiple of
     8 elements apart); more keys than queries is a chunk behind a cached prefix.  No sequence may
     have more queries than max_query_len or more keys than max_key_len."""
-    torch = _torch()
-    dev = _place(q, "q")
-    if q.dim() != 3 or key.dim() != 3 or key.shape[1] != num_kv_heads or query_start.dim() != 1:
-        raise ValueError("q [T, Hq, D], key [Tk, num_kv_heads, D] and query_start [S + 1] expected")
-    T, Hq, D = q.shape
-    Tk, Hkv, _ = key.shape
-    dt = q.dtype
-    code = _dtype_code(q)
-    qp, qs = _rows(q, "q", dt, (T, Hq, D), dev)
-    k, ks = _rows(key, "key", dt, (Tk, Hkv, D), dev)
-    v, vs = _rows(value, "value", dt, (Tk, Hkv, D), dev)
-    S = max(0, query_start.shape[0] - 1)
-    o = _flat(out, "out", dt, (T, Hq, D), dev)
-    starts = (_flat(query_start, "query_start", torch.int32, (S + 1,), dev),
-              _flat(key_start, "key_start", torch.int32, (S + 1,), dev))
-    L = lib()
-    if workspace is None:
-        need = L.pa_prompt_attention_workspace_bytes(S, T, Hq, Hkv, D, max_query_len, max_key_len)
-        if need:
-            workspace = _scratch(need, q, stream)
-    wp, wb = (None, 0) if workspace is None else _bytes(workspace, dev)
-    st = L.pa_prompt_attention(o, qp, k, v, *starts, scale, Hkv, S, T, Tk, Hq, D, max_query_len,
-                               max_key_len, qs, ks, vs, code, wp, wb, _on(stream, dev))
+    st = _native().prompt(out, q, key, value, query_start, key_start, scale, num_kv_heads,
+                           max_query_len, max_key_len, workspace, _raw(stream))
     if st:
         _check(st, "pa_prompt_attention")
     return out

@@ -1,5 +1,6 @@
-"""Build libpa.so in-tree: every CUDA kernel for sm_100a plus the host block
-manager, one shared library exposing the C ABI of include/pa.h.
+"""Build in-tree: libpa.so, every CUDA kernel for sm_100a plus the host block
+manager, one shared library exposing the C ABI of include/pa.h; and _calls, the
+extension module that marshals torch tensors for the shortest calls.
 
     python -m paged_kv_cache_414_b200.build [--force] [--verbose]
 """
@@ -9,12 +10,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libpa.so")
+CALLS = os.path.join(PKG, "_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 CU_SOURCES = ["pa_kernels.cu"]
@@ -39,14 +42,41 @@ def _inputs():
     return files
 
 
+def _newer(out, inputs) -> bool:
+    return os.path.exists(out) and all(os.path.getmtime(f) <= os.path.getmtime(out)
+                                       for f in inputs)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    return _newer(LIB, _inputs())
+
+
+def build_calls(force: bool = False) -> str:
+    """The extension module, against the headers of the installed torch."""
+    src = os.path.join(CSRC, "binding.cpp")
+    if not force and _newer(CALLS, [src, os.path.join(INCLUDE, "pa.h")]):
+        return CALLS
+    import torch
+    home = os.path.dirname(torch.__file__)
+    inc = os.path.join(home, "include")
+    lib = os.path.join(home, "lib")
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    tmp = CALLS + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(cuda, "include"), src, "-o", tmp, "-L", lib,
+           "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
+    os.replace(tmp, CALLS)
+    return CALLS
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_calls(force)
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)
