@@ -9,7 +9,9 @@
 // Work split as in the 16-bit decode kernel (decode_attention.cuh): the tiles of
 // all (sequence, kv head) pairs, numbered in order, are cut into equal
 // contiguous ranges, one per warp, and cut segments leave partials for the
-// merge kernel.  Every warp finds its range by itself.  Here a tile is 32 tokens
+// merge kernel.  Every warp finds its range by itself.  Where no context can be
+// longer than a few tiles, ranges are cut between pairs only and there is
+// nothing to merge.  Here a tile is 32 tokens
 // whatever the block size (two blocks of 16 or one of 32): half the bytes per
 // token would otherwise leave twice the bookkeeping per byte.  Every kv head of
 // a sequence begins with a tile of no tokens that stands for what a segment
@@ -79,7 +81,7 @@ struct DecodeFp8Params {
   int num_seqs, num_q_heads, num_kv_heads, group;
   int max_blocks, num_blocks, block_size;
   int q_bf16;
-  int min_tiles;                 // fewest tiles a warp is given
+  int min_tiles;                 // fewest tiles a warp is given; 0: whole (sequence, kv head) pairs
   uint64_t wait_ns;              // limit of a wait on a copy before giving up (2 s by default)
 };
 
@@ -559,60 +561,80 @@ __global__ void __launch_bounds__(NW * 32, fp8_ctas(NT, HPL))
   grid_dependency_wait();
   allow_dependent_launch();
 
-  // ---- this warp's range: lane l counts the tiles (of one kv head) of
-  // sequences per * l ..
   const int w_total = gridDim.x * NW, w = blockIdx.x * NW + warp;
-  const int per = (S + 31) / 32;
-  int mine = 0;
-#pragma unroll 8
-  for (int k = 0; k < per; ++k) {
-    const int s = lane * per + k;
-    mine += s < S ? fp8_tiles(fp8_length(p, s)) : 0;
-  }
-  int total;
-  const int before = warp_scan(mine, lane, &total);
-  const long long U = (long long)total * p.num_kv_heads;
-  const int w_active = (int)min((long long)w_total, (U + p.min_tiles - 1) / p.min_tiles);
   // empty sequences' rows, and lengths that the table cannot hold
   for (int s = w; s < S; s += w_total) {
     const int L = __ldg(p.context_lens + s);
     if (lane == 0 && (L < 0 || L > p.max_blocks * B)) flag_error(PA_DEVERR_CONTEXT_LEN);
-    if (L <= 0 || p.max_blocks == 0) {
+    if (L <= 0) {
       float4 *row = reinterpret_cast<float4 *>(p.out + (int64_t)s * p.num_q_heads * D);
       for (int k = lane; k < p.num_q_heads * D / 4; k += 32) row[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
-  if (w >= w_active) {
-    if (lane == 0) p.meta[w] = make_int4(0, 0, 0, 0);
-    return;
-  }
-  const long long u01 = (long long)(w + (lane & 1)) * U / w_active;
-  const long long u0 = __shfl_sync(0xffffffffu, u01, 0), u1 = __shfl_sync(0xffffffffu, u01, 1);
-  const int ntiles = (int)(u1 - u0);
-  // the sequence that tile u0 belongs to: first the lane that counted it, then
-  // that lane's sequences 32 at a time
-  const int t0 = (int)(u0 / p.num_kv_heads);
-  const int owner =
-      31 - __clz(__ballot_sync(0xffffffffu, before <= t0));   // the last one that begins before
-  int s0 = owner * per, base = __shfl_sync(0xffffffffu, before, owner), L0 = 0;
-  for (int k0 = 0; k0 < per; k0 += 32) {
-    const int s = owner * per + k0 + lane;
-    const int L = k0 + lane < per && s < S ? fp8_length(p, s) : 0;
-    int sum;
-    const int at = base + warp_scan(fp8_tiles(L), lane, &sum);
-    if (base + sum <= t0) {
-      base += sum;
-      continue;
+  // ---- this warp's range: ntiles tiles from tile j0 of kv head h0 of sequence s0 on
+  int s0, h0, j0, L0, nt0, ntiles, w_active = 0;
+  long long u0 = 0, U = 0;
+  if (p.min_tiles == 0) {
+    const long long pairs = (long long)S * p.num_kv_heads;
+    const long long a = pairs * w / w_total, e = pairs * (w + 1) / w_total;
+    int sum = 0;
+    for (long long i = a + lane; i < e; i += 32)
+      sum += fp8_tiles(fp8_length(p, (int)(i / p.num_kv_heads)));
+    ntiles = __reduce_add_sync(0xffffffffu, sum);
+    if (ntiles == 0) return;
+    s0 = (int)(a / p.num_kv_heads);
+    h0 = (int)(a - (long long)s0 * p.num_kv_heads);
+    j0 = 0;
+    L0 = fp8_length(p, s0);
+    nt0 = fp8_tiles(L0);
+  } else {
+    // lane l counts the tiles (of one kv head) of sequences per * l ..
+    const int per = (S + 31) / 32;
+    int mine = 0;
+#pragma unroll 8
+    for (int k = 0; k < per; ++k) {
+      const int s = lane * per + k;
+      mine += s < S ? fp8_tiles(fp8_length(p, s)) : 0;
     }
-    const int hit = 31 - __clz(__ballot_sync(0xffffffffu, at <= t0));
-    s0 = owner * per + k0 + hit;
-    base = __shfl_sync(0xffffffffu, at, hit);
-    L0 = __shfl_sync(0xffffffffu, L, hit);
-    break;
+    int total;
+    const int before = warp_scan(mine, lane, &total);
+    U = (long long)total * p.num_kv_heads;
+    w_active = (int)min((long long)w_total, (U + p.min_tiles - 1) / p.min_tiles);
+    if (w >= w_active) {
+      if (lane == 0) p.meta[w] = make_int4(0, 0, 0, 0);
+      return;
+    }
+    const long long u01 = (long long)(w + (lane & 1)) * U / w_active;
+    u0 = __shfl_sync(0xffffffffu, u01, 0);
+    ntiles = (int)(__shfl_sync(0xffffffffu, u01, 1) - u0);
+    // the sequence that tile u0 belongs to: first the lane that counted it, then
+    // that lane's sequences 32 at a time
+    const int t0 = (int)(u0 / p.num_kv_heads);
+    const int owner =
+        31 - __clz(__ballot_sync(0xffffffffu, before <= t0));   // the last one that begins before
+    int base = __shfl_sync(0xffffffffu, before, owner);
+    s0 = owner * per;
+    L0 = 0;
+    for (int k0 = 0; k0 < per; k0 += 32) {
+      const int s = owner * per + k0 + lane;
+      const int L = k0 + lane < per && s < S ? fp8_length(p, s) : 0;
+      int sum;
+      const int at = base + warp_scan(fp8_tiles(L), lane, &sum);
+      if (base + sum <= t0) {
+        base += sum;
+        continue;
+      }
+      const int hit = 31 - __clz(__ballot_sync(0xffffffffu, at <= t0));
+      s0 = owner * per + k0 + hit;
+      base = __shfl_sync(0xffffffffu, at, hit);
+      L0 = __shfl_sync(0xffffffffu, L, hit);
+      break;
+    }
+    nt0 = fp8_tiles(L0);
+    const long long r0 = u0 - (long long)base * p.num_kv_heads;
+    h0 = (int)(r0 / nt0);
+    j0 = (int)(r0 - (long long)h0 * nt0);
   }
-  const int nt0 = fp8_tiles(L0);
-  const long long r0 = u0 - (long long)base * p.num_kv_heads;
-  const int h0 = (int)(r0 / nt0), j0 = (int)(r0 - (long long)h0 * nt0);
 
   // ---- the walk, and the copies of a tile
   Fp8Walk walk;
@@ -683,7 +705,7 @@ __global__ void __launch_bounds__(NW * 32, fp8_ctas(NT, HPL))
   // inside a segment and no earlier one does, the segment's (sequence, kv
   // head), its first partial and the number of them; the others are the first
   // partials of the ranges behind the first
-  {
+  if (p.min_tiles > 0) {
     const long long lo = u0 - j0, hi = lo + nt0;
     // the range that holds tile u: the largest c with c U / w_active <= u
     const long long c01 = (((lane & 1) ? hi : lo + 1) * w_active - 1) / U;
@@ -738,8 +760,9 @@ __global__ void __launch_bounds__(NW * 32, fp8_ctas(NT, HPL))
 // ============================================================================
 // Merge of split segments.  A warp looks at `span` ranges (one per lane) and
 // merges the segments that are first cut at one of them, GMW heads at a time:
-// with many segments about every range begins inside one, with few long ones
-// a segment has many partials and the heads go to different warps.
+// with many segments about every range begins inside one.  With few long ones
+// (GMW = 1) a segment has many partials: each head goes to a CTA, whose four
+// warps share the partials.
 // ============================================================================
 template <int D, int GMW>
 __global__ void __launch_bounds__(128)
@@ -749,7 +772,10 @@ __global__ void __launch_bounds__(128)
   using VecT = typename std::conditional<VPL == 4, float4, float2>::type;
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 5);
+  constexpr bool kShare = GMW == 1;
+  __shared__ float joined[kShare ? 4 : 1][D + 2];   // each warp's sums, their maximum and weight
+  const int warp = threadIdx.x >> 5;
+  const int t = kShare ? blockIdx.x : blockIdx.x * 4 + warp;
   const int G = p.group, g0 = t % groups * GMW, b = t / groups * span + lane;
   const int4 mine = lane < span && b < w_total ? __ldcg(p.meta + b) : make_int4(0, 0, 0, 0);
   unsigned todo = __ballot_sync(0xffffffffu, mine.w > 0);
@@ -768,7 +794,7 @@ __global__ void __launch_bounds__(128)
 #pragma unroll
       for (int v = 0; v < VPL; ++v) num[g][v] = 0.f;
     }
-    for (int k0 = 0; k0 < n; k0 += 32) {
+    for (int k0 = kShare ? warp * 32 : 0; k0 < n; k0 += kShare ? 128 : 32) {
       const int k = k0 + lane, cnt = min(n - k0, 32);
       const bool ok = k < n;
       const long long row = (long long)(k == 0 ? first : 2 * (c_lo + k)) * G + g0;
@@ -822,6 +848,27 @@ __global__ void __launch_bounds__(128)
           }
         }
       }
+    }
+    if constexpr (kShare) {
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) joined[warp][lane * VPL + v] = num[0][v];
+      if (lane == 0) joined[warp][D] = M[0], joined[warp][D + 1] = den[0];
+      __syncthreads();
+      float top = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) top = fmaxf(top, joined[k][D]);
+      den[0] = 0.f;
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) num[0][v] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {   // (a warp without partials: a maximum of -inf)
+        const float wk = joined[k][D] == -INFINITY ? 0.f : exp2f(joined[k][D] - top);
+        den[0] = fmaf(wk, joined[k][D + 1], den[0]);
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) num[0][v] = fmaf(wk, joined[k][lane * VPL + v], num[0][v]);
+      }
+      __syncthreads();
+      if (warp > 0) continue;
     }
     float *dst = p.out + ((int64_t)sh * G + g0) * D + lane * VPL;
 #pragma unroll

@@ -155,7 +155,7 @@ bool encode_code_map(CUtensorMap *m, const void *base, long long rows, int D, in
 
 template <int D, int NT, int HPL>
 int launch_decode_fp8(pa::DecodeFp8Params &p, const CUtensorMap &kmap, const CUtensorMap &vmap,
-                      uint8_t *workspace, size_t workspace_bytes, int dev, int sms,
+                      uint8_t *workspace, size_t workspace_bytes, int max_context, int dev, int sms,
                       cudaStream_t stream) {
   auto kern = pa::paged_decode_fp8_kernel<D, NT, HPL, kWarpsPerCta>;
   const int G = p.group;
@@ -169,26 +169,41 @@ int launch_decode_fp8(pa::DecodeFp8Params &p, const CUtensorMap &kmap, const CUt
       return PA_ERR_CUDA;
     attr_set[dev].store(smem);
   }
-  const int grid = sms * ctas, w_total = grid * kWarpsPerCta;
+  const long long pairs = (long long)p.num_seqs * p.num_kv_heads;
+  const long long tiles = (max_context + pa::kF8Tile - 1) / pa::kF8Tile + 1;   // of a pair, at most
+  // Short contexts are not cut (a warp takes a pair's tiles in less time than a
+  // cut, its partials and the merge cost): up to 64 tokens (one sequence of 40
+  // tokens, 32 / 8 heads: 7.4 us whole, 8.7 cut), or 128 where the pairs alone
+  // give every eighth warp work (128 sequences of 128: 13.2 and 16.8; but one
+  // of 128: 10.3 and 8.7, 128 of 512: 34.2 and 34.0).  Else at least two tiles
+  // to a warp, or one where that still leaves warps without work (one sequence
+  // of 256: 9.3 us with one, 10.4 with two, 13.2 with four).
+  const int mt = g_tune_min_tiles.load();
+  const long long most_warps = (long long)sms * ctas * kWarpsPerCta;
+  const bool whole = tiles <= 3 || (tiles <= 5 && pairs * 8 >= most_warps);
+  p.min_tiles = mt > 0 ? mt : (whole ? 0 : (pairs * tiles * 2 <= most_warps && tiles <= 64 ? 1 : 2));
+  // No more warps than can have work.
+  const long long useful = p.min_tiles == 0 ? pairs : (pairs * tiles + p.min_tiles - 1) / p.min_tiles;
+  const int grid = (int)std::min<long long>((useful + kWarpsPerCta - 1) / kWarpsPerCta,
+                                            (long long)sms * ctas);
+  const int w_total = grid * kWarpsPerCta;
   size_t off_ml, off_o;
   if (workspace_bytes < workspace_for(w_total, G, D, &off_ml, &off_o)) return PA_ERR_WORKSPACE;
   p.meta = reinterpret_cast<int4 *>(workspace);
   p.part_ml = reinterpret_cast<float2 *>(workspace + off_ml);
   p.part_o = reinterpret_cast<float *>(workspace + off_o);
-  const int mt = g_tune_min_tiles.load();
-  p.min_tiles = mt > 0 ? mt : 4;
   if (launch_dependent(kern, dim3(grid), kWarpsPerCta * 32, smem, stream, kmap, vmap, p) !=
       cudaSuccess)
     return PA_ERR_CUDA;
+  if (p.min_tiles == 0) return PA_OK;   // nothing was cut
   // Segments are at least as many as (sequence, kv head) pairs, cuts at most as
   // many as ranges: with many pairs a warp takes one range and four heads, else
-  // as many ranges as there are to a pair, and one head.
-  const long long pairs = (long long)p.num_seqs * p.num_kv_heads;
+  // a CTA as many ranges as there are to a pair, and one head.
   int span = 1;
   while (span < 32 && pairs * span * 2 <= w_total) span *= 2;
   const int heads = span > 1 ? 1 : 4, groups = (G + heads - 1) / heads;
   const long long warps = (long long)((w_total + span - 1) / span) * groups;
-  const dim3 mgrid((unsigned)((warps + 3) / 4));
+  const dim3 mgrid((unsigned)(span > 1 ? warps : (warps + 3) / 4));
   const cudaError_t e =
       span > 1 ? launch_dependent(pa::paged_decode_fp8_merge_kernel<D, 1>, mgrid, 128, 0, stream, p,
                                   w_total, span, groups)
@@ -375,8 +390,10 @@ int pa_paged_decode_attention_fp8(float *out, const void *q, const void *k_cache
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   cudaStream_t st = (cudaStream_t)stream;
   return head_dim == 128
-             ? dispatch_decode_fp8<128>(p, kmap, vmap, ws, workspace_bytes, dev, sms, st)
-             : dispatch_decode_fp8<64>(p, kmap, vmap, ws, workspace_bytes, dev, sms, st);
+             ? dispatch_decode_fp8<128>(p, kmap, vmap, ws, workspace_bytes, max_context_len, dev,
+                                        sms, st)
+             : dispatch_decode_fp8<64>(p, kmap, vmap, ws, workspace_bytes, max_context_len, dev,
+                                        sms, st);
 }
 
 int pa_copy_blocks_fp8(void *k_cache, void *v_cache, float *kv_scale, const int64_t *block_mapping,
