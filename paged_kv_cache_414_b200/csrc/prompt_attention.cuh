@@ -41,6 +41,8 @@ struct PromptParams {
   const int32_t *key_start;    // [S + 1]
   float *part_o;               // [units][pieces][256][D], keys split only
   float2 *part_ml;             // [units][pieces][256]  (max in log2 units, sum)
+  int4 *part_of;               // [units]  first token, tokens, parts of tiles A and B (tokens
+                               // negative: of one query tile, see PromptUnit::alternate)
   float scale_log2;            // scale * log2(e)
   int num_seqs, num_tokens, num_key_tokens, num_q_heads, num_kv_heads, group;
   int tq;                      // tokens per query tile
@@ -60,6 +62,9 @@ constexpr int kPrConsumers = 11;   // warps that read a unit's description
 // A unit as the scheduler describes it.
 struct PromptUnit {
   int n[2];        // K/V tiles of query tiles A and B in this piece; n[0] < 0: no more units
+  int tiles;       // K/V tiles in all
+  int alternate;   // there is only tile A, and B stands for it too: A takes the even K/V tiles,
+                   // B the odd ones, each with a partial of its own
   int first_key;   // global row of the piece's first key
   int token0;      // global row of tile A's first token
   int tokens;      // of tiles A and B
@@ -342,13 +347,31 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             const int j0 = piece * p.piece_tiles;
             u.n[0] = min(max(w.tiles[0] - j0, 0), p.piece_tiles);
             u.n[1] = min(max(w.tiles[1] - j0, 0), p.piece_tiles);
+            u.tiles = max(u.n[0], u.n[1]);
+            u.alternate = p.pieces > 1 && w.tokens <= p.tq;
+            if (u.alternate) {
+              u.n[1] = u.n[0] / 2;
+              u.n[0] -= u.n[1];
+            }
             u.first_key = w.key0 + j0 * kPrKeys;
             u.token0 = w.token0;
             u.tokens = w.tokens;
             u.pos0 = w.pos0 - j0 * kPrKeys;
             u.kv_head = kh;
             u.slot = block;
-            give = u.n[0] > 0 || u.n[1] > 0 || p.pieces == 1;   // no keys: rows of zeros
+            give = u.tiles > 0 || p.pieces == 1;   // no keys: rows of zeros
+            if (p.pieces > 1 && piece == 0 && lane == 0) {
+              // what the join needs: parts with keys (of the last one's two, B's
+              // has none if it is one tile long)
+              const int parts[2] = {(w.tiles[0] + p.piece_tiles - 1) / p.piece_tiles,
+                                    (w.tiles[1] + p.piece_tiles - 1) / p.piece_tiles};
+              p.part_of[rest] =
+                  u.alternate ? make_int4(w.token0, -w.tokens, parts[0],
+                                          parts[0] - (w.tiles[0] % p.piece_tiles == 1))
+                              : make_int4(w.token0, w.tokens, parts[0], parts[1]);
+            }
+          } else if (p.pieces > 1 && piece == 0 && lane == 0) {
+            p.part_of[rest] = make_int4(0, 0, 0, 0);
           }
         }
         if (give) {
@@ -386,8 +409,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       int it = 0, loads = 0, vloads = 0, nq = 0;   // K/V tiles, units with a Q
       bool ok = true;
       while (ok && next_unit(u)) {
-        const int nm = max(u.n[0], u.n[1]);
-        for (int j = 0; ok && j < nm; ++j, ++it) {
+        for (int j = 0; ok && j < u.tiles; ++j, ++it) {
           const int st = it % NST;
           const uint32_t free_phase = (it / NST - 1) & 1;
           if (it >= NST && !(ok = wait_all(&empty_k[st], free_phase))) break;
@@ -439,8 +461,9 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       const uint64_t dK0 = umma_desc_sw128(smem_addr(sK), 16, 1024);
       const uint64_t dV0 = umma_desc_sw128(smem_addr(sV), kPrKeys * 128, 1024);
       constexpr uint32_t kStageStep = L::KV_BYTES >> 4, kQStep = L::Q_TILE >> 4;
+      bool alternate = false;
       auto issue_s = [&](int x, int st) {       // S_x = Q_x K^T
-        const uint64_t dq = dQ0 + x * kQStep, dk = dK0 + st * kStageStep;
+        const uint64_t dq = dQ0 + (alternate ? 0 : x) * kQStep, dk = dK0 + st * kStageStep;
         const uint32_t d = tmem + x * 256;
         constexpr uint32_t kRegion = L::REGION >> 4;
         if constexpr (D == 128)
@@ -465,51 +488,58 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       unsigned it = 0, p_phase = 0;             // p_phase bit x: parity of the P awaited from tile x
       int nq = 0, nclean = 0;
       bool ok = true;
+      // O_x += P_x V of one tile, as its two halves come
+      auto add_pv = [&](int x, int st, bool first) {
+        const uint32_t parity = (p_phase >> x) & 1;
+        p_phase ^= 1u << x;
+        if (!wait_all(&p_half[x], parity)) return false;
+        tc_fence_after();
+        issue_pv0(x, st, first);
+        if (!wait_all(&p_full[x], parity)) return false;
+        tc_fence_after();
+        issue_pv1(x, st);
+        return true;
+      };
       while (ok && next_unit(u)) {
-        const int nm = max(u.n[0], u.n[1]);
+        const int nm = u.tiles;
         if (nm == 0) continue;
         const bool tail = u.pos0 + u.tokens < nm * kPrKeys;   // keys behind the last position
-        ok = wait_all(&q_full, nq & 1) && wait_all(&full_k[it % NST], (it / NST) & 1);
-        if (!ok) break;
+        alternate = u.alternate;
+        ok = wait_all(&q_full, nq & 1);
         ++nq;
-        tc_fence_after();
+        // step j: P.V of K/V tile j and the scores that then have room -- tile
+        // j + 1's of both query tiles, or tile j + 2's of the one whose turn it is
+        const int ahead = alternate ? 2 : 1;
 #pragma unroll 1
-        for (int x = 0; x < 2; ++x)
-          if ((x ? u.n[1] : u.n[0]) > 0) issue_s(x, it % NST);
-        umma_commit(&empty_k[it % NST]);
-        if (nm == 1) umma_commit(&q_empty);
-        for (int j = 0; ok && j < nm; ++j, ++it) {
-          const int st = it % NST, sn = (it + 1) % NST;
-          const bool more = j + 1 < nm;
-          ok = wait_all(&full_v[st], (it / NST) & 1);
-          if (ok && tail && !more) {
-            if (lane == 0) mbar_arrive(&v_tail);
-            ok = wait_all(&v_clean, nclean++ & 1);
+        for (int j = -ahead; ok && j < nm; ++j) {
+          const unsigned tv = it + j, tk = tv + ahead;
+          const int st = tv % NST, sn = tk % NST;
+          const bool more = j + ahead < nm;
+          if (j >= 0) {
+            ok = wait_all(&full_v[st], (tv / NST) & 1);
+            if (ok && tail && j + 1 == nm) {
+              if (lane == 0) mbar_arrive(&v_tail);
+              ok = wait_all(&v_clean, nclean++ & 1);
+            }
           }
-          if (ok && more) ok = wait_all(&full_k[sn], ((it + 1) / NST) & 1);
-          if (!ok) break;
+          if (ok && more) ok = wait_all(&full_k[sn], (tk / NST) & 1);
 #pragma unroll 1
-          for (int x = 0; x < 2; ++x) {
-            const int n = x ? u.n[1] : u.n[0];
-            if (j >= n) continue;
-            const uint32_t parity = (p_phase >> x) & 1;
-            p_phase ^= 1u << x;
-            ok = wait_all(&p_half[x], parity);
-            if (!ok) break;
+          for (int x = 0; ok && x < 2; ++x) {
+            if (alternate ? x != (j & 1) : j >= (x ? u.n[1] : u.n[0])) continue;
+            if (j >= 0) {
+              ok = add_pv(x, st, j < ahead);
+              if (!ok) break;
+            }
             tc_fence_after();
-            issue_pv0(x, st, j == 0);
-            ok = wait_all(&p_full[x], parity);
-            if (!ok) break;
-            tc_fence_after();
-            issue_pv1(x, st);
-            if (j + 1 == n) umma_commit(&o_done[x]);
-            else issue_s(x, sn);
+            if (alternate ? more : j + 1 < (x ? u.n[1] : u.n[0])) issue_s(x, sn);
+            else if (j >= 0) umma_commit(&o_done[x]);
           }
           if (!ok) break;
-          umma_commit(&empty_v[st]);
+          if (j >= 0) umma_commit(&empty_v[st]);
           if (more) umma_commit(&empty_k[sn]);
-          if (j + 2 == nm) umma_commit(&q_empty);
+          if (j + ahead + 1 == nm) umma_commit(&q_empty);
         }
+        it += nm;
       }
       umma_commit(&drain);
       mbar_wait_bounded(&drain, 0, kPfDrainLimitNs);
@@ -520,7 +550,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       PromptUnit u;
       int it = 0, asked = 0;
       while (next_unit(u)) {
-        const int nm = max(u.n[0], u.n[1]);
+        const int nm = u.tiles;
         it += nm;
         const int live = u.pos0 + u.tokens - (nm - 1) * kPrKeys;   // rows of the last tile that count
         if (nm == 0 || live >= kPrKeys) continue;
@@ -550,9 +580,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     bool ok = true;
     while (ok && next_unit(u)) {
       const int n = x ? u.n[1] : u.n[0];
-      const bool row_ok = t < p.tq && x * p.tq + t < u.tokens;
-      const int pos = row_ok ? u.pos0 + x * p.tq + t : u.pos0 + u.tokens - 1;
-      const int pos_min = u.pos0 + x * p.tq;
+      const int tx = u.alternate ? 0 : x * p.tq;               // the query tile's first token
+      const bool row_ok = t < p.tq && tx + t < u.tokens;
+      const int pos = row_ok ? u.pos0 + tx + t : u.pos0 + u.tokens - 1;
+      const int pos_min = u.pos0 + tx;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j, ++ns) {
         ok = wait_all(&s_full[x], ns & 1);
@@ -560,8 +591,9 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         tc_fence_after();
         // keys past a row's position, and a scale that is not positive: the
         // scores are first rewritten where they lie
-        const int lim = pos - j * kPrKeys;                     // keys 0 .. lim of the tile count
-        const bool masked = pos_min < j * kPrKeys + kPrKeys - 1;
+        const int first = (u.alternate ? 2 * j + x : j) * kPrKeys;   // the tile's first key
+        const int lim = pos - first;                           // keys 0 .. lim of the tile count
+        const bool masked = pos_min < first + kPrKeys - 1;
         if (masked || !pos_scale) {
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
@@ -654,11 +686,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           for (int c = 0; c < D; c += 16) {
             uint32_t o[16];
             tmem_load16(tO + c, o);
-            if (row_ok)
-#pragma unroll
-              for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<uint4 *>(dst + c + i) =
-                    make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            if (row_ok) {
+              st_global_v8(dst + c, o);
+              st_global_v8(dst + c + 8, o + 8);
+            }
           }
           if (row_ok) p.part_ml[row] = make_float2(m, l);
         }
@@ -666,7 +697,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         const bool none = l == 0.f;          // nothing seen: zeros, whatever V holds
         const float inv = 1.f / l;
         T *dst = static_cast<T *>(p.out) +
-                 ((long long)(u.token0 + x * p.tq + t) * p.num_q_heads + u.kv_head * G + r - t * G) * D;
+                 ((long long)(u.token0 + tx + t) * p.num_q_heads + u.kv_head * G + r - t * G) * D;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32], h[16];
@@ -700,68 +731,82 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   }
 }
 
-// Join of the pieces of the keys: a CTA takes 32 rows of one (pair of query
-// tiles, kv head), a warp one row at a time, each lane D / 32 columns.
+// Join of the pieces of the keys: a warp takes one of the 256 rows of a (pair
+// of query tiles, kv head), each lane D / 32 columns.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptParams p) {
-  constexpr int VPL = D / 32;
-  __shared__ int2 seqs[kPrSeqCache];
-  __shared__ int found[2];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int VPL = D / 32, UNR = 8;
+  using VecT = typename std::conditional<VPL == 4, float4, float2>::type;
   grid_dependency_wait();
   allow_dependent_launch();
-  const int kh = blockIdx.x % p.num_kv_heads, v = blockIdx.x / p.num_kv_heads;
-  if (warp == 0) {
-    for (int i = lane; i < min(p.num_seqs, kPrSeqCache); i += 32) seqs[i] = prompt_seq(p, i, false);
-    __syncwarp();
-    int s = -1, pair = 0;
-    if (!prompt_find(p, seqs, v, s, pair)) s = -1;
-    if (lane == 0) found[0] = s, found[1] = pair;
-  }
-  __syncthreads();
-  if (found[0] < 0) return;
-  const PromptPair u = prompt_pair(p, found[0], found[1]);
-  for (int k = 0; k < 4; ++k) {
-    const int row = blockIdx.y * 32 + warp * 4 + k;   // of the pair's 256
-    const int x = row >> 7, r = row & 127, t = r / p.group, g = r - t * p.group;
-    if (t >= p.tq || x * p.tq + t >= u.tokens) continue;
-    const int n = (u.tiles[x] + p.piece_tiles - 1) / p.piece_tiles;
-    const long long first = ((long long)blockIdx.x * p.pieces) * 256 + row;
-    float M = -INFINITY, den = 0.f, num[VPL];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.y * 8 + warp, x = row >> 7, r = row & 127;
+  const int t = r / p.group, g = r - t * p.group;
+  const int4 of = __ldcg(p.part_of + blockIdx.x);
+  const bool alternate = of.y < 0;
+  const int token = x * p.tq + t;
+  if (t >= p.tq || token >= abs(of.y) || (alternate && x > 0) || of.x < 0 ||
+      of.x + token >= p.num_tokens)
+    return;
+  // part i of the row's: of its own query tile, then (alternate) of B's rows
+  const int own = min(x ? of.w : of.z, p.pieces), n = own + (alternate ? min(of.w, p.pieces) : 0);
+  const long long first = (long long)blockIdx.x * p.pieces * 256 + row;
+  float M = -INFINITY, den = 0.f, num[VPL];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) num[i] = 0.f;
-    for (int i = 0; i < n; ++i) {
-      const float2 ml = __ldcg(p.part_ml + first + (long long)i * 256);
-      const float mn = fmax3_nan(M, ml.x, ml.x);
-      const float ref = mn == -INFINITY ? 0.f : mn;
-      const float a = exp2f(M - ref), b = exp2f(ml.x - ref);
-      const float *src = p.part_o + (first + (long long)i * 256) * D + lane * VPL;
-      den = den * a + ml.y * b;
-      if constexpr (VPL == 4) {
-        const float4 o = __ldcg(reinterpret_cast<const float4 *>(src));
-        num[0] = num[0] * a + o.x * b, num[1] = num[1] * a + o.y * b;
-        num[2] = num[2] * a + o.z * b, num[3] = num[3] * a + o.w * b;
-      } else {
-        const float2 o = __ldcg(reinterpret_cast<const float2 *>(src));
-        num[0] = num[0] * a + o.x * b, num[1] = num[1] * a + o.y * b;
+  for (int v = 0; v < VPL; ++v) num[v] = 0.f;
+  for (int k0 = 0; k0 < n; k0 += 32) {
+    const int k = k0 + lane, cnt = min(n - k0, 32);
+    const long long at = first + (k < own ? (long long)k * 256 : (long long)(k - own) * 256 + 128);
+    const float2 ml = k < n ? __ldcg(p.part_ml + at) : make_float2(-INFINITY, 0.f);
+    // the largest so far; a NaN goes along
+    float top = ml.x;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      const float y = __shfl_xor_sync(0xffffffffu, top, d);
+      top = fmax3_nan(top, y, y);
+    }
+    top = fmax3_nan(top, M, M);
+    const float ref = top == -INFINITY ? 0.f : top;
+    const float keep = exp2f(M - ref), wk = exp2f(ml.x - ref);   // no keys seen: 0
+    float sum = wk * ml.y;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    den = den * keep + sum;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) num[v] *= keep;
+    M = top;
+    for (int j0 = 0; j0 < cnt; j0 += UNR) {
+      VecT o[UNR];
+#pragma unroll
+      for (int j = 0; j < UNR; ++j) {
+        const long long aj = __shfl_sync(0xffffffffu, at, min(j0 + j, cnt - 1));
+        o[j] = __ldcg(reinterpret_cast<const VecT *>(p.part_o + aj * D) + lane);
       }
-      M = mn;
-    }
-    if (M == -INFINITY) {             // nothing seen: zeros, whatever V holds
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) num[i] = 0.f;
-      den = 1.f;
+      for (int j = 0; j < UNR; ++j) {
+        if (j0 + j >= cnt) break;
+        const float wj = __shfl_sync(0xffffffffu, wk, j0 + j);
+        num[0] = fmaf(wj, o[j].x, num[0]);
+        num[1] = fmaf(wj, o[j].y, num[1]);
+        if constexpr (VPL == 4) {
+          num[2] = fmaf(wj, o[j].z, num[2]);
+          num[3] = fmaf(wj, o[j].w, num[3]);
+        }
+      }
     }
-    const float inv = 1.f / den;
-    T *dst = static_cast<T *>(p.out) +
-             ((long long)(u.token0 + x * p.tq + t) * p.num_q_heads + kh * p.group + g) * D +
-             lane * VPL;
-    if constexpr (VPL == 4)
-      *reinterpret_cast<uint2 *>(dst) = make_uint2(Mma<T>::pack(num[0] * inv, num[1] * inv),
-                                                   Mma<T>::pack(num[2] * inv, num[3] * inv));
-    else
-      *reinterpret_cast<uint32_t *>(dst) = Mma<T>::pack(num[0] * inv, num[1] * inv);
   }
+  const bool none = M == -INFINITY;   // nothing seen: zeros, whatever V holds
+  const float inv = 1.f / den;
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) num[v] = none ? 0.f : num[v] * inv;
+  const int kh = blockIdx.x % p.num_kv_heads;
+  T *dst = static_cast<T *>(p.out) +
+           ((long long)(of.x + token) * p.num_q_heads + kh * p.group + g) * D + lane * VPL;
+  if constexpr (VPL == 4)
+    *reinterpret_cast<uint2 *>(dst) =
+        make_uint2(Mma<T>::pack(num[0], num[1]), Mma<T>::pack(num[2], num[3]));
+  else
+    *reinterpret_cast<uint32_t *>(dst) = Mma<T>::pack(num[0], num[1]);
 }
 
 }  // namespace pa

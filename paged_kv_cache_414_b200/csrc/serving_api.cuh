@@ -245,6 +245,10 @@ struct PromptPlan {
   size_t workspace;
 };
 
+// The keys are split if that takes at least so many K/V tiles off the longest
+// CTA's way: partials and their join cost what about ten tiles do.
+constexpr long long kSplitGain = 12;
+
 PromptPlan plan_prompt(int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads,
                        int head_dim, int max_query, int max_key, int sms) {
   PromptPlan pl;
@@ -257,13 +261,14 @@ PromptPlan plan_prompt(int num_seqs, int num_tokens, int num_q_heads, int num_kv
   pl.pieces = 1;
   pl.piece_tiles = (int)tiles;
   if (pl.units < sms) {
-    const long long per = std::max(4ll, (pl.units * tiles + 2 * sms - 1) / (2 * sms));
-    if (per < tiles) {
+    const long long per = std::max(2ll, (pl.units * tiles + sms - 1) / sms);
+    if (per + kSplitGain <= tiles) {
       pl.piece_tiles = (int)per;
       pl.pieces = (int)((tiles + per - 1) / per);
     }
   }
-  pl.workspace = pl.pieces > 1 ? (size_t)pl.units * pl.pieces * 256 * (head_dim * 4 + 8) : 0;
+  pl.workspace =
+      pl.pieces > 1 ? (size_t)pl.units * (pl.pieces * 256ll * (head_dim * 4 + 8) + 16) : 0;
   return pl;
 }
 
@@ -296,7 +301,7 @@ int launch_prompt(pa::PromptParams &p, const PromptPlan &pl, const CUtensorMap &
                        qmap, kmap, vmap, p) != cudaSuccess)
     return PA_ERR_CUDA;
   if (pl.pieces > 1 &&
-      launch_dependent(pa::prompt_join_kernel<T, D>, dim3((unsigned)pl.units, 8), 256, 0, stream,
+      launch_dependent(pa::prompt_join_kernel<T, D>, dim3((unsigned)pl.units, 32), 256, 0, stream,
                        p) != cudaSuccess)
     return PA_ERR_CUDA;
   return PA_OK;
@@ -539,6 +544,7 @@ int pa_prompt_attention(void *out, const void *q, const void *key, const void *v
   p.part_o = static_cast<float *>(workspace);
   p.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) +
                                          (size_t)pl.units * pl.pieces * 256 * head_dim * 4);
+  p.part_of = reinterpret_cast<int4 *>(p.part_ml + pl.units * pl.pieces * 256);
   p.scale_log2 = scale * 1.4426950408889634f;
   p.num_seqs = num_seqs;
   p.num_tokens = num_tokens;
