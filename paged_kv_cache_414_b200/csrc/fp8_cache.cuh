@@ -46,9 +46,10 @@ struct RopeParams {
 // 8l .. 8l+7 in either order and both its loads and its 16-bit stores are
 // 16-byte vectors; a row's amax is a shuffle among its lanes.
 //
-// A warp takes a token's heads 512 / D at a time, so that the cosines and sines
-// of its lanes are fetched once per token; a pass's rows are loaded two passes
-// ahead, the next token's positions and slot a token ahead.  With few tokens `splits` warps share one.  Bound: HBM; 16384
+// A warp takes a token's heads 512 / D at a time -- the query heads, then K's
+// and V's -- so that the cosines and sines of its lanes are fetched once per
+// token; a pass's rows are loaded two passes ahead, the next token's positions
+// and slot a token ahead.  With few tokens `splits` warps share one.  Bound: HBM; 16384
 // tokens of 32 q and 8 kv heads took 119 us with four heads to a thread and no
 // loop (15 warps per SM, all waiting for the same things at the same time).
 template <typename T, int D, bool FP8, bool PAIRS>
@@ -57,7 +58,8 @@ __global__ void __launch_bounds__(256, 3) rope_and_cache_kernel(const RopeParams
   grid_dependency_wait();
   allow_dependent_launch();
   const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
-  const int nq = p.num_q_heads, nk = nq + p.num_kv_heads, nv = nk + p.num_kv_heads;
+  const int nq = p.num_q_heads, nkv = p.num_kv_heads;
+  const int pq = (nq + HPP - 1) / HPP, all = pq + (2 * nkv + HPP - 1) / HPP;   // passes of a token
   const int units = p.num_tokens * p.splits, step = gridDim.x * 8;
   int unit = blockIdx.x * 8 + (threadIdx.x >> 5);
 
@@ -97,23 +99,25 @@ __global__ void __launch_bounds__(256, 3) rope_and_cache_kernel(const RopeParams
     }
     const long long blk = keep ? slot / p.block_size : 0;
     const int off = keep ? (int)(slot - blk * p.block_size) : 0;
-    const int first = part * p.passes * HPP + sub;          // this lane's first head
+    const int p0 = part * p.passes, p1 = min(p0 + p.passes, all);
 
+    const T *qrow = static_cast<const T *>(p.q) + t * p.q_stride + sub * D;
+    const T *krow = static_cast<const T *>(p.k) + t * p.k_stride;
+    const T *vrow = static_cast<const T *>(p.v) + t * p.v_stride;
     uint4 x0[2], x1[2];                                     // the next two passes' rows
-    auto load = [&](int h, uint4 (&y)[2]) {
+    auto load = [&](int ps, uint4 (&y)[2]) {
       const T *row = nullptr;
-      if (h < nq)
-        row = static_cast<const T *>(p.q) + t * p.q_stride + (long long)h * D;
-      else if (h < nk)
-        row = static_cast<const T *>(p.k) + t * p.k_stride + (long long)(h - nq) * D;
-      else if (h < nv)
-        row = static_cast<const T *>(p.v) + t * p.v_stride + (long long)(h - nk) * D;
+      if (ps < min(pq, p1)) {
+        if (ps * HPP + sub < nq) row = qrow + ps * (HPP * D);
+      } else if (ps < p1) {
+        const int h = (ps - pq) * HPP + sub;
+        if (h < 2 * nkv) row = h < nkv ? krow + h * D : vrow + (h - nkv) * D;
+      }
       y[0] = row ? *reinterpret_cast<const uint4 *>(row + e0) : make_uint4(0, 0, 0, 0);
       y[1] = row ? *reinterpret_cast<const uint4 *>(row + e1) : make_uint4(0, 0, 0, 0);
     };
-    const int passes = min(p.passes, (nv - part * p.passes * HPP + HPP - 1) / HPP);
-    load(first, x0);
-    load(passes > 1 ? first + HPP : nv, x1);                // (nv: no row)
+    load(p0, x0);
+    load(p0 + 1, x1);
 
     float c[8], s[8];
     const long long pos = __shfl_sync(0xffffffffu, now, axis0);
@@ -139,9 +143,8 @@ __global__ void __launch_bounds__(256, 3) rope_and_cache_kernel(const RopeParams
       }
     }
 
-    auto finish = [&](int h, const uint4 (&y)[2]) {
-      const bool is_q = h < nq, is_k = !is_q && h < nk, is_v = !is_q && !is_k && h < nv;
-      float f[16];   // columns e0 .. e0+7, then e1 .. e1+7
+    // columns e0 .. e0+7, then e1 .. e1+7, turned if `turn`
+    auto unpack = [&](const uint4 (&y)[2], bool turn, float (&f)[16]) {
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         const uint32_t g[4] = {y[w].x, y[w].y, y[w].z, y[w].w};
@@ -152,7 +155,7 @@ __global__ void __launch_bounds__(256, 3) rope_and_cache_kernel(const RopeParams
           f[8 * w + 2 * m + 1] = v2.y;
         }
       }
-      if (!is_v && turns) {
+      if (turn) {
 #pragma unroll
         for (int m = 0; m < 8; ++m) {
           const int ia = PAIRS ? 2 * m : m, ib = PAIRS ? 2 * m + 1 : m + 8;
@@ -161,14 +164,51 @@ __global__ void __launch_bounds__(256, 3) rope_and_cache_kernel(const RopeParams
           f[ib] = b * c[m] + a * s[m];
         }
       }
-      if (FP8 && __any_sync(0xffffffffu, h >= nq)) {   // some K or V row in this pass
+    };
+    auto store16 = [&](T *row, const float (&f)[16]) {
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+        *reinterpret_cast<uint4 *>(row + (w ? e1 : e0)) =
+            make_uint4(Mma<T>::pack(f[8 * w], f[8 * w + 1]),
+                       Mma<T>::pack(f[8 * w + 2], f[8 * w + 3]),
+                       Mma<T>::pack(f[8 * w + 4], f[8 * w + 5]),
+                       Mma<T>::pack(f[8 * w + 6], f[8 * w + 7]));
+    };
+    int ps = p0;
+    T *qout = static_cast<T *>(p.q_out) + t * p.q_out_stride + sub * D;
+#pragma unroll 1
+    for (; ps < min(pq, p1); ++ps) {
+      const uint4 y[2] = {x0[0], x0[1]};
+      x0[0] = x1[0], x0[1] = x1[1];
+      load(ps + 2, x1);
+      float f[16];
+      unpack(y, turns, f);
+      if (ps * HPP + sub < nq) store16(qout + ps * (HPP * D), f);
+    }
+    // rows of the pool: K or V head h of this token
+    const long long tile0 = blk * nkv;
+#pragma unroll 1
+    for (; ps < p1; ++ps) {
+      const uint4 y[2] = {x0[0], x0[1]};
+      x0[0] = x1[0], x0[1] = x1[1];
+      load(ps + 2, x1);
+      const int h = (ps - pq) * HPP + sub;
+      const bool is_k = h < nkv;
+      const long long tile = tile0 + (is_k ? h : h - nkv);
+      const long long row = tile * p.block_size + off;
+      const bool put = keep && h < 2 * nkv;
+      float f[16];
+      unpack(y, turns && is_k, f);
+      if constexpr (!FP8) {
+        if (put) store16(static_cast<T *>(is_k ? p.k_cache : p.v_cache) + row * D, f);
+      } else {
         float amax = 0.f;
 #pragma unroll
         for (int m = 0; m < 16; ++m) amax = fmaxf(amax, fabsf(f[m]));
 #pragma unroll
         for (int d = 1; d < LPR; d <<= 1)
           amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-        if (keep && (is_k || is_v)) {
+        if (put) {
           const float top = fmaxf(amax, kLeastAmax);
           const float inv = kE4m3Max / top;
           uint32_t w4[4];
@@ -180,37 +220,12 @@ __global__ void __launch_bounds__(256, 3) rope_and_cache_kernel(const RopeParams
                 make_float2(f[4 * m + 2] * inv, f[4 * m + 3] * inv), __NV_SATFINITE, __NV_E4M3);
             w4[m] = (uint32_t)lo | ((uint32_t)hi << 16);
           }
-          const long long tile = blk * p.num_kv_heads + (is_k ? h - nq : h - nk);
-          uint8_t *row = static_cast<uint8_t *>(is_k ? p.k_cache : p.v_cache) +
-                         (tile * p.block_size + off) * D;
-          *reinterpret_cast<uint2 *>(row + e0) = make_uint2(w4[0], w4[1]);
-          *reinterpret_cast<uint2 *>(row + e1) = make_uint2(w4[2], w4[3]);
-          if (l == 0)
-            p.kv_scale[(tile * 2 + (is_k ? 0 : 1)) * p.block_size + off] = top / kE4m3Max;
+          uint8_t *dst = static_cast<uint8_t *>(is_k ? p.k_cache : p.v_cache) + row * D;
+          *reinterpret_cast<uint2 *>(dst + e0) = make_uint2(w4[0], w4[1]);
+          *reinterpret_cast<uint2 *>(dst + e1) = make_uint2(w4[2], w4[3]);
+          if (l == 0) p.kv_scale[(tile * 2 + (is_k ? 0 : 1)) * p.block_size + off] = top / kE4m3Max;
         }
       }
-      T *row = nullptr;
-      if (is_q)
-        row = static_cast<T *>(p.q_out) + t * p.q_out_stride + (long long)h * D;
-      else if (!FP8 && keep && (is_k || is_v))
-        row = static_cast<T *>(is_k ? p.k_cache : p.v_cache) +
-              ((blk * p.num_kv_heads + (is_k ? h - nq : h - nk)) * p.block_size + off) * D;
-      if (row) {
-#pragma unroll
-        for (int w = 0; w < 2; ++w)
-          *reinterpret_cast<uint4 *>(row + (w ? e1 : e0)) =
-              make_uint4(Mma<T>::pack(f[8 * w], f[8 * w + 1]),
-                         Mma<T>::pack(f[8 * w + 2], f[8 * w + 3]),
-                         Mma<T>::pack(f[8 * w + 4], f[8 * w + 5]),
-                         Mma<T>::pack(f[8 * w + 6], f[8 * w + 7]));
-      }
-    };
-#pragma unroll 1
-    for (int i = 0; i < passes; ++i) {
-      const uint4 y[2] = {x0[0], x0[1]};
-      x0[0] = x1[0], x0[1] = x1[1];
-      load(i + 2 < passes ? first + (i + 2) * HPP : nv, x1);
-      finish(first + i * HPP, y);
     }
   }
 }

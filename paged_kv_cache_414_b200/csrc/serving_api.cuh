@@ -37,7 +37,7 @@ cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, int threads, siz
 template <typename T, int D, bool FP8, bool PAIRS>
 int launch_rope(pa::RopeParams &p, int sms, cudaStream_t stream) {
   constexpr int HPP = 512 / D;   // heads of a pass
-  const int heads = p.num_q_heads + 2 * p.num_kv_heads, all = (heads + HPP - 1) / HPP;
+  const int all = (p.num_q_heads + HPP - 1) / HPP + (2 * p.num_kv_heads + HPP - 1) / HPP;
   // As many warps to a token as leave every SM its 24, one pass each at most.
   const long long resident = 24ll * sms;
   p.splits = (int)std::max(1ll, std::min<long long>(all, resident / p.num_tokens));
@@ -466,7 +466,7 @@ int pa_gather_cache_fp8(void *key, void *value, const void *k_cache, const void 
   const int chunks = (num_tokens + pa::kGatherRows - 1) / pa::kGatherRows;
   const int rows = 2 * num_kv_heads * pa::kGatherRows, groups = 256 / (head_dim / 16);
   const int most = (rows + groups - 1) / groups;
-  const int split = std::max(1, std::min(most, 8 * sms / chunks));
+  const int split = std::max(1, std::min(most, 16 * sms / chunks));
   const dim3 grid(chunks, std::min(split, 65535));
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e;
