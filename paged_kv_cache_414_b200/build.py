@@ -20,9 +20,9 @@ LIB = os.path.join(PKG, "libpa.so")
 CALLS = os.path.join(PKG, "_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 BUILD_DIR = os.path.join(ROOT, "_build")
 
-CU_SOURCES = ["pa_kernels.cu"]
+CU_SOURCES = ["library.cu"]
 CPP_SOURCES = ["block_manager.cpp"]
-HEADERS = sorted(f for f in os.listdir(CSRC) if f.endswith((".cuh", ".h")))
+HEADERS = sorted(f for f in os.listdir(CSRC) if f.endswith((".cuh", ".cu", ".h")))
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",

@@ -15,9 +15,6 @@
 #include "cache_ops.cuh"
 #include "decode_attention.cuh"
 #include "prefill_attention.cuh"
-#include "fp8_cache.cuh"
-#include "decode_fp8.cuh"
-#include "prompt_attention.cuh"
 
 namespace {
 
@@ -569,6 +566,3 @@ int pa_decode_tuning(int nstage, int ctas_per_sm, int min_tiles_per_warp) {
 }
 
 }  // extern "C"
-
-// Operators around the 8-bit cache and the prompt pass.
-#include "serving_api.cuh"

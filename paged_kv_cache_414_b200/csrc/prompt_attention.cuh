@@ -32,6 +32,7 @@
 #pragma once
 
 #include "prefill_attention.cuh"
+#include "prompt_umma.cuh"
 
 namespace pa {
 
@@ -293,6 +294,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     abort_flag = 0;
     fence_barrier_init();
   }
+  if (threadIdx.x == 32) {
+    prefetch_tensormap(&qmap);
+    prefetch_tensormap(&kmap);
+    prefetch_tensormap(&vmap);
+  }
   if (warp == 9) {
     tmem_alloc(&tmem_slot, kPfTmemCols);
     tmem_relinquish();
@@ -400,11 +406,6 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       }
     } else if (warp == 8) {
       // ------------------------------------------------------------ producer
-      if (lane == 0) {
-        prefetch_tensormap(&qmap);
-        prefetch_tensormap(&kmap);
-        prefetch_tensormap(&vmap);
-      }
       PromptUnit u;
       int it = 0, loads = 0, vloads = 0, nq = 0;   // K/V tiles, units with a Q
       bool ok = true;
