@@ -388,7 +388,9 @@ int pa_rope_and_cache_fp8(void *q_out, const void *q, const void *key, const voi
  * pa_paged_decode_attention over the 8-bit pool: the same arguments, masks,
  * workspace (pa_paged_decode_workspace_bytes) and errors, plus kv_scale; q of
  * dtype, out fp32.  Accumulated in fp32 with the weights carried to 2^-22, so
- * the output is that of the cached values (code * scale) to ~1e-6.
+ * the output is that of the cached values (code * scale) to ~1e-6.  Of
+ * pa_decode_tuning the CTAs per SM and the tiles per warp apply; contexts that
+ * max_context_len says are short are not split at all.
  */
 int pa_paged_decode_attention_fp8(float *out, const void *q, const void *k_cache,
                                   const void *v_cache, const float *kv_scale,
@@ -415,8 +417,8 @@ int pa_copy_blocks_fp8(void *k_cache, void *v_cache, float *kv_scale, const int6
  *   key, value    dtype [num_tokens, num_kv_heads, head_dim] (device, written)
  *   block_tables  int32 [num_seqs, max_blocks_per_seq] (device)
  *   key_start     int32 [num_seqs + 1] (device), non-decreasing
- * Rows from key_start[num_seqs] on are left as they were.  A position beyond
- * the table sets PA_DEVERR_CONTEXT_LEN, a block id outside the pool
+ * Rows before key_start[0] and from key_start[num_seqs] on are left as they
+ * were.  A position beyond the table sets PA_DEVERR_CONTEXT_LEN, a block id outside the pool
  * PA_DEVERR_BLOCK_ID; their rows are left as they were.
  */
 int pa_gather_cache_fp8(void *key, void *value, const void *k_cache, const void *v_cache,

@@ -279,7 +279,7 @@ struct GatherParams {
 // counted by all threads at once (one load deep, no search), the others
 // follow from it; then K and V of every head, in an order that reads a
 // block's tokens of one head one after the other.  gridDim.y splits the
-// heads.  Rows behind the last sequence are left as they are.
+// heads.  Rows before the first sequence and behind the last are left as they are.
 constexpr int kGatherRows = 16;
 template <typename T, int D>
 __global__ void __launch_bounds__(256) gather_cache_fp8_kernel(const GatherParams p) {
@@ -301,9 +301,9 @@ __global__ void __launch_bounds__(256) gather_cache_fp8_kernel(const GatherParam
     long long c = -1;
     if (r < p.num_tokens && s < p.num_seqs) {
       const long long pos = (long long)r - __ldg(p.key_start + s);
-      if (pos < 0 || pos >= (long long)p.max_blocks * p.block_size) {
+      if (pos >= (long long)p.max_blocks * p.block_size) {
         flag_error(PA_DEVERR_CONTEXT_LEN);
-      } else {
+      } else if (pos >= 0) {   // (rows before the first sequence are no one's)
         const int blk = __ldg(p.block_tables + (long long)s * p.max_blocks + pos / p.block_size);
         if (blk < 0 || blk >= p.num_blocks)
           flag_error(PA_DEVERR_BLOCK_ID);

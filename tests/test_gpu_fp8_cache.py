@@ -404,6 +404,17 @@ def test_gather(pa, dtype, Hkv, D, B):
         assert (got[T:] == 7).all()
 
 
+def test_gather_leaves_rows_of_no_sequence(pa):
+    k, v, sc = make_pool(6, 2, 16, 64, seed=34)
+    tables = torch.tensor([[4, 1]], dtype=torch.int32, device="cuda")
+    key, value = (torch.full((60, 2, 64), 7.0, dtype=torch.float16, device="cuda") for _ in range(2))
+    pa.pa_gather_cache_fp8(key, value, k, v, sc, tables, torch.tensor([9, 40], dtype=torch.int32, device="cuda"))
+    want = rows_of(k, sc, 0, tables[0], 31, 16)
+    assert ((key[9:40].double() - want).abs() <= (2.0 ** -11 + 2 * U32) * want.abs() + 2.0 ** -25).all()
+    for got in (key, value):
+        assert (got[:9] == 7).all() and (got[40:] == 7).all()
+
+
 def test_gather_bad_tables_are_flagged(pa):
     k, v, sc = make_pool(6, 2, 16, 64, seed=33)
     tables = torch.tensor([[0, 6], [2, 3]], dtype=torch.int32, device="cuda")
@@ -514,3 +525,29 @@ def test_captured_and_replayed_on_another_stream(pa):
     for x, y in zip((kc, vc), eager):
         assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
     assert torch.equal(sc, eager[2])
+
+
+def test_two_calls_at_once_on_two_streams(pa):
+    """Decode calls on two streams, each with the workspace the binding makes for it, between
+    allocations that would reuse that memory too early."""
+    B, Hkv, D, S = 16, 8, 128, 64
+    lens = [(97 * i) % 1500 for i in range(S)]
+    NB = sum(-(-n // B) for n in lens)
+    k, v, sc = make_pool(NB, Hkv, B, D, seed=71)
+    tables = make_tables(lens, B, NB, 72)
+    ctx = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q = [torch.randn(S, 32, D, generator=generator(i), device="cuda").bfloat16() for i in (1, 2)]
+    want = [torch.empty(S, 32, D, device="cuda") for _ in q]
+    for a, b in zip(want, q):
+        pa.pa_paged_decode_attention_fp8(a, b, k, v, sc, tables, ctx, D ** -0.5, Hkv)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in q]
+    got = [[torch.zeros_like(want[0]) for _ in range(6)] for _ in q]
+    torch.cuda.synchronize()
+    for r in range(6):
+        for i, st in enumerate(streams):
+            pa.pa_paged_decode_attention_fp8(got[i][r], q[i], k, v, sc, tables, ctx, D ** -0.5, Hkv, stream=st)
+            torch.full((4 << 20,), float("nan"), device="cuda")      # on the current stream
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, want[i]) for x in got[i])

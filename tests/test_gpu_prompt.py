@@ -107,6 +107,53 @@ def test_few_queries_many_keys(pa, dtype, Hq, Hkv, D):
     check(out, C, L, q, k, v, D ** -0.5)
 
 
+@pytest.mark.parametrize("L", [1792, 1793, 2049, 2176, 2177, 4000])
+def test_one_query_tile_and_odd_tiles(pa, L):
+    """One query tile takes the K/V tiles in turn with itself; the last piece may hold one tile,
+    and another sequence's queries may stand before its first key."""
+    C, L = [3, 8], [L, 5]
+    q, k, v = inputs(C, L, 4, 1, 128, torch.bfloat16, seed=31)
+    assert pa.lib().pa_prompt_attention_workspace_bytes(2, 11, 4, 1, 128, 8, L[0]) > 0
+    check(run(pa, C, L, q, k, v, 0.09), C, L, q, k, v, 0.09)
+
+
+def test_output_on_any_16_bytes(pa):
+    """An output that begins in the middle of a 32-byte sector."""
+    C = [200, 70]
+    q, k, v = inputs(C, C, 4, 2, 64, torch.float16, seed=32)
+    out = torch.full((q.numel() + 8,), 7.0, dtype=q.dtype, device="cuda")[8:].view(q.shape)
+    assert out.data_ptr() % 32 == 16
+    check(run(pa, C, C, q, k, v, 0.125, out=out), C, C, q, k, v, 0.125)
+
+
+def test_large_values(pa):
+    """bf16 values far outside fp16's range."""
+    C = [150]
+    q, k, v = inputs(C, C, 4, 2, 64, torch.bfloat16, seed=33)
+    v *= 1e30
+    q, k = q * 1e8, k * 1e-8
+    out = run(pa, C, C, q, k, v, 0.125)
+    check_sequence(out, q, k, v, 0.125)
+
+
+def test_two_streams(pa):
+    """Split calls on two streams at once, workspaces from the binding."""
+    C, L = [5, 9], [6000, 3000]
+    a, b = (inputs(C, L, 16, 2, 128, torch.bfloat16, seed=i) for i in (41, 42))
+    want = [run(pa, C, L, *x, 0.09) for x in (a, b)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for r in range(5):
+        for i, x in enumerate((a, b)):
+            out = torch.full_like(x[0], 7.0)
+            streams[i].wait_stream(torch.cuda.current_stream())
+            got[i].append(run(pa, C, L, *x, 0.09, out=out, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, want[i]) for x in got[i])
+
+
 def test_larger_bounds_than_lengths(pa):
     """max_query_len and max_key_len may be anything that covers the lengths."""
     C, L = [100, 37], [300, 37]
