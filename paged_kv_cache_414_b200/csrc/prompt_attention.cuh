@@ -112,40 +112,51 @@ __device__ __forceinline__ bool prompt_wait(uint64_t *bar, uint32_t parity, vola
 
 // ---------------------------------------------------------------- units
 
-// What the numbering needs of a sequence: units are its pairs of query tiles,
-// pair i has order e0 + i, which grows with the keys it sees.
-__device__ __forceinline__ int2 prompt_seq(const PromptParams &p, int s, bool report) {
+// A sequence: its first query and key rows and how many; no queries if it is not
+// one that can be computed.
+struct PromptSeq {
+  int q0, C, k0, L;
+};
+__device__ __forceinline__ PromptSeq prompt_seq(const PromptParams &p, int s, bool report) {
   const int q0 = __ldg(p.query_start + s), q1 = __ldg(p.query_start + s + 1);
   const int k0 = __ldg(p.key_start + s), k1 = __ldg(p.key_start + s + 1);
   if (q0 < 0 || q1 < q0 || q1 > p.num_tokens || k0 < 0 || k1 < k0 || k1 > p.num_key_tokens ||
       q1 - q0 > p.max_query || k1 - k0 > p.max_key) {
     if (report) flag_error(PA_DEVERR_CONTEXT_LEN);
-    return make_int2(0, 0);
+    return PromptSeq{0, 0, 0, 0};
   }
-  const int w = 2 * p.tq;
-  return make_int2(max(0, (k1 - k0) - (q1 - q0)) / w, (q1 - q0 + w - 1) / w);
+  return PromptSeq{q0, q1 - q0, k0, k1 - k0};
 }
 
-// Unit number v in order of decreasing length (ties by sequence): its sequence
-// and pair, or false past the last one.  A whole warp; `cache` holds the first
-// kPrSeqCache sequences' prompt_seq.
-__device__ __forceinline__ bool prompt_find(const PromptParams &p, const int2 *cache, int v, int &s,
-                                            int &pair) {
+// What the numbering needs of it: units are its pairs of query tiles (y of
+// them), pair i has order x + i, which grows with the keys it sees.
+__device__ __forceinline__ int2 prompt_order(const PromptParams &p, const PromptSeq &q) {
+  const int w = 2 * p.tq;
+  return make_int2(max(0, q.L - q.C) / w, (q.C + w - 1) / w);
+}
+
+// Unit number v in order of decreasing length (ties by sequence): its pair and
+// sequence, or false past the last one.  A whole warp; lane i holds sequence i
+// and its order, the further ones' orders are in `cache` as far as that goes.
+__device__ __forceinline__ bool prompt_find(const PromptParams &p, const int2 *cache,
+                                            const PromptSeq &mine, int2 order, int v,
+                                            PromptSeq *found, int *pair) {
   const int lane = threadIdx.x & 31;
-  auto seq = [&](int i) {
-    return i < kPrSeqCache ? cache[i] : prompt_seq(p, i, false);
+  auto further = [&](int i) {
+    return i < kPrSeqCache ? cache[i] : prompt_order(p, prompt_seq(p, i, false));
   };
   auto at_least = [&](int e) {   // units of order e or more
-    int n = 0;
+    int n = min(max(order.x + order.y - e, 0), order.y);
 #pragma unroll 1
-    for (int i = lane; i < p.num_seqs; i += 32) {
-      const int2 q = seq(i);
+    for (int i = lane + 32; i < p.num_seqs; i += 32) {
+      const int2 q = further(i);
       n += min(max(q.x + q.y - e, 0), q.y);
     }
     return __reduce_add_sync(0xffffffffu, n);
   };
   // at_least(lo) > v >= at_least(hi) = above, once lo is known not to be -1
   int lo = -1, hi = (p.max_query + p.max_key) / (2 * p.tq) + 2, above = 0;
+  if (p.num_seqs <= 32) hi = __reduce_max_sync(0xffffffffu, order.x + order.y);
 #pragma unroll 1
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1, n = at_least(mid);
@@ -161,16 +172,23 @@ __device__ __forceinline__ bool prompt_find(const PromptParams &p, const int2 *c
 #pragma unroll 1
   for (int i0 = 0; i0 < p.num_seqs; i0 += 32) {
     const int i = i0 + lane;
-    const int2 q = i < p.num_seqs ? seq(i) : make_int2(0, 0);
+    const int2 q = i0 == 0 ? order : (i < p.num_seqs ? further(i) : make_int2(0, 0));
     const bool has = q.x <= lo && lo < q.x + q.y;
     const unsigned who = __ballot_sync(0xffffffffu, has);
     const int many = __popc(who);
     if (left < many) {
-      const unsigned mine = __ballot_sync(
+      const unsigned which = __ballot_sync(
           0xffffffffu, has && __popc(who & ((1u << lane) - 1u)) == left);
-      const int src = __ffs(mine) - 1;
-      s = i0 + src;
-      pair = lo - __shfl_sync(0xffffffffu, q.x, src);
+      const int src = __ffs(which) - 1;
+      *pair = lo - __shfl_sync(0xffffffffu, q.x, src);
+      if (i0 == 0) {
+        found->q0 = __shfl_sync(0xffffffffu, mine.q0, src);
+        found->C = __shfl_sync(0xffffffffu, mine.C, src);
+        found->k0 = __shfl_sync(0xffffffffu, mine.k0, src);
+        found->L = __shfl_sync(0xffffffffu, mine.L, src);
+      } else {
+        *found = prompt_seq(p, i0 + src, false);
+      }
       return true;
     }
     left -= many;
@@ -186,15 +204,14 @@ struct PromptPair {
   int token0, tokens, pos0, key0;
   int tiles[2];   // of A and B over the whole length
 };
-__device__ __forceinline__ PromptPair prompt_pair(const PromptParams &p, int s, int pair) {
-  const int q0 = __ldg(p.query_start + s), C = __ldg(p.query_start + s + 1) - q0;
-  const int k0 = __ldg(p.key_start + s), L = __ldg(p.key_start + s + 1) - k0;
+__device__ __forceinline__ PromptPair prompt_pair(const PromptParams &p, const PromptSeq &q,
+                                                  int pair) {
   PromptPair u;
   const int t0 = pair * 2 * p.tq;
-  u.token0 = q0 + t0;
-  u.tokens = min(2 * p.tq, C - t0);
-  u.pos0 = L - C + t0;
-  u.key0 = k0;
+  u.token0 = q.q0 + t0;
+  u.tokens = min(2 * p.tq, q.C - t0);
+  u.pos0 = q.L - q.C + t0;
+  u.key0 = q.k0;
   u.tiles[0] = prompt_tiles(u.pos0 + min(p.tq, u.tokens) - 1);
   u.tiles[1] = u.tokens > p.tq ? prompt_tiles(u.pos0 + u.tokens - 1) : 0;
   return u;
@@ -332,12 +349,15 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == 10) {
       // ------------------------------------------------------------ scheduler
+      const PromptSeq mine =
+          lane < p.num_seqs ? prompt_seq(p, lane, blockIdx.x == 0) : PromptSeq{0, 0, 0, 0};
+      const int2 order = prompt_order(p, mine);
 #pragma unroll 1
-      for (int i = lane; i < min(p.num_seqs, kPrSeqCache); i += 32)
-        seqs[i] = prompt_seq(p, i, blockIdx.x == 0);
-      if (blockIdx.x == 0)
-#pragma unroll 1
-        for (int i = kPrSeqCache + lane; i < p.num_seqs; i += 32) prompt_seq(p, i, true);
+      for (int i = lane + 32; i < p.num_seqs; i += 32) {
+        if (i >= kPrSeqCache && blockIdx.x != 0) break;   // (one CTA reports)
+        const int2 q = prompt_order(p, prompt_seq(p, i, blockIdx.x == 0));
+        if (i < kPrSeqCache) seqs[i] = q;
+      }
       __syncwarp();
       int block = blockIdx.x, made = 0, asked = 0;
       while (true) {
@@ -347,9 +367,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         if (block >= 0) {
           const int piece = block % p.pieces, rest = block / p.pieces;
           const int kh = rest % p.num_kv_heads, v = rest / p.num_kv_heads;
-          int s, pair;
-          if (prompt_find(p, seqs, v, s, pair)) {
-            const PromptPair w = prompt_pair(p, s, pair);
+          PromptSeq q;
+          int pair;
+          if (prompt_find(p, seqs, mine, order, v, &q, &pair)) {
+            const PromptPair w = prompt_pair(p, q, pair);
             const int j0 = piece * p.piece_tiles;
             u.n[0] = min(max(w.tiles[0] - j0, 0), p.piece_tiles);
             u.n[1] = min(max(w.tiles[1] - j0, 0), p.piece_tiles);
@@ -571,7 +592,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int x = warp >> 2;                 // query tile
     const int r = threadIdx.x & 127;         // this thread's row, and lane of tensor memory
-    const int t = r / G;
+    const int t = r / G, t_lo = (r - lane) / G;
     const uint32_t tS = tmem + x * 256 + ((uint32_t)((warp & 3) * 32) << 16), tO = tS + 128;
     const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
     const bool pos_scale = p.scale_log2 > 0.f;
@@ -584,7 +605,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       const int tx = u.alternate ? 0 : x * p.tq;               // the query tile's first token
       const bool row_ok = t < p.tq && tx + t < u.tokens;
       const int pos = row_ok ? u.pos0 + tx + t : u.pos0 + u.tokens - 1;
-      const int pos_min = u.pos0 + tx;
+      const int pos_lo = u.pos0 + tx + t_lo;                   // of this warp's first row
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j, ++ns) {
         ok = wait_all(&s_full[x], ns & 1);
@@ -594,10 +615,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         // scores are first rewritten where they lie
         const int first = (u.alternate ? 2 * j + x : j) * kPrKeys;   // the tile's first key
         const int lim = pos - first;                           // keys 0 .. lim of the tile count
-        const bool masked = pos_min < first + kPrKeys - 1;
-        if (masked || !pos_scale) {
+        // of its four runs of 32 keys, every row of this warp sees those before `whole`
+        const int whole = max((pos_lo - first + 1) >> 5, 0);
+        if (whole < 4 || !pos_scale) {
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+          for (int c = pos_scale ? whole : 0; c < 4; ++c) {
             uint32_t w[32];
             tmem_load32(tS + c * 32, w);
 #pragma unroll
@@ -652,15 +674,14 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int k = c * 32 + 2 * i, s = (i & 1) * 2;
-            float x0, x1, p0, p1;
+            float x0, x1;
             ffma2(x0, x1, __uint_as_float(v[k]), __uint_as_float(v[k + 1]), sl2, sl2, -ref, -ref);
-            p0 = fast_exp2(x0);
-            p1 = fast_exp2(x1);
+            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
             fadd2(sum[s], sum[s + 1], sum[s], sum[s + 1], p0, p1);
             h[i] = Mma<T>::pack(p0, p1);
           }
           tmem_store16_async(tS + c * 16, h);
-          if (c == 1) {          // P.V may begin on the first half
+          if (c == 1) {              // P.V may begin on the first half
             tmem_store_wait();
             tc_fence_before();
             __syncwarp();
