@@ -1,8 +1,9 @@
 """Python binding of libpa.so, the B200 paged-KV-cache attention library.
 
 Argument marshalling only: every function here (the shortest calls through the
-extension module _calls) checks the torch tensors it is given, passes their device pointers, sizes and the current CUDA stream to the
-C ABI declared in include/pa.h, and raises on a non-zero status.  No step of
+extension module _calls) checks the torch tensors it is given, passes their
+device pointers, sizes and the current CUDA stream to the C ABI declared in
+include/pa.h, and raises on a non-zero status.  No step of
 the computation runs in Python, and there is no fallback: if libpa.so is
 missing or a call fails, an exception is raised.
 
@@ -12,7 +13,8 @@ the fused ``pa_decode_step``, ``pa_paged_prefill_attention`` (chunked prefill),
 ``pa_copy_blocks``, ``pa_device_error``, ``pa_decode_tuning``, ``pa_set_wait_limit``;
 rotary positions with the cache write, ``pa_rope_and_cache``; the 8-bit pool's
 ``pa_rope_and_cache_fp8``, ``pa_paged_decode_attention_fp8``, ``pa_gather_cache_fp8``
-and ``pa_copy_blocks_fp8``; attention over packed prompts, ``pa_prompt_attention``; and the host block manager ``BlockManager`` over the ``pa_bm_*`` calls (prefix
+and ``pa_copy_blocks_fp8``; attention over packed prompts, ``pa_prompt_attention``;
+and the host block manager ``BlockManager`` over the ``pa_bm_*`` calls (prefix
 caching included).
 """
 from __future__ import annotations

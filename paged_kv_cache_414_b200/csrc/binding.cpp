@@ -283,6 +283,10 @@ int rope(PyObject *const *args, Py_ssize_t n) {
     }
   }
   const int turn = PyObject_IsTrue(c.object(11));
+  if (turn < 0) {
+    PyErr_Clear();
+    throw Refused{PyExc_TypeError, "interleaved must be true or false"};
+  }
   const cudaStream_t st = c.stream(12);
   if (fp8)
     return entry.rope_fp8(q_out, q, k, v, p.k, p.v, p.scale, slots, pos, table, sect, n32(axes),

@@ -28,8 +28,8 @@
 // Arithmetic.
 //   * Codes become fp16 exactly (cvt.rn.f16x2.e4m3x2) and both products are
 //     fp16 warp MMAs (m16n8k16, fp32 accumulation) for fp16 and bf16 queries
-//     alike.  (The e4m3 warp MMA on e4m3 pieces of the queries was built too:
-//     the decode of 256 mixed sequences took 103 us with it, 97 with this.)
+//     alike.  (With the e4m3 warp MMA on e4m3 pieces of the queries the decode
+//     of 256 mixed sequences took 6 percent longer.)
 //   * A query row is scaled by the power of two that puts its largest element
 //     in [2^14, 2^15) before it is rounded to fp16: exact for fp16 queries and
 //     for bf16 elements down to 2^-39 of the row's largest.
@@ -48,8 +48,8 @@
 // (g, c) takes D/4 neighbouring codes of K row g, and D/8 neighbouring columns
 // of V for its four tokens; bytes of two tokens are paired with one byte
 // permute before the conversion.  Chunks are swizzled within 128-byte (D = 128)
-// or 64-byte (D = 64) rows, with which the K loads and D = 128's V loads are free of bank
-// conflicts.
+// or 64-byte (D = 64) rows, with which the K loads and D = 128's V loads are
+// free of bank conflicts.
 //
 // Bound: HBM, 2 D + 8 bytes per token and kv head.
 #pragma once

@@ -29,6 +29,17 @@
 // weights (2^-9 or 2^-12 each, independent) costs about as much as rounding
 // the output does.  Maximum, sum and O are fp32.  O is rescaled only when a
 // row's maximum grows by more than 2^8 (weights then stay below 2^8).
+//
+// Bound: the chain of a tile's softmax between its two products, at half of the
+// tensor cores' rate (the exponentials' unit is busy for as long).  One prompt
+// of 8192 tokens, 32 / 8 heads of 128: 459 us, 1.2 PFLOP/s of visible pairs;
+// 16 prompts of 64 to 2048 tokens, 40 heads: 209 us, 0.69 (their units have few
+// tiles, and the diagonal ones count half).  Measured and left: a polynomial on the FMA units for a
+// quarter of the exponentials (498 us), scores in halves of 64 keys with two in
+// flight (590), two threads to a row (783), the next unit's first scores before
+// this one's last P.V (465), heads in groups whose K/V fit the L2 cache (as
+// before or slower), masks as selects in registers instead of a pass over the
+// tile (457, with spills).
 #pragma once
 
 #include "prefill_attention.cuh"
@@ -418,7 +429,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         }
         __syncwarp();
         if (!wait_all(&answer_bar, asked & 1)) {
-          mbar_wait_bounded(&answer_bar, asked & 1, kPfDrainLimitNs);   // it lands before the CTA exits
+          // it lands before the CTA exits
+          mbar_wait_bounded(&answer_bar, asked & 1, kPfDrainLimitNs);
           break;
         }
         ++asked;
@@ -574,7 +586,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       while (next_unit(u)) {
         const int nm = u.tiles;
         it += nm;
-        const int live = u.pos0 + u.tokens - (nm - 1) * kPrKeys;   // rows of the last tile that count
+        // rows of the last tile that count
+        const int live = u.pos0 + u.tokens - (nm - 1) * kPrKeys;
         if (nm == 0 || live >= kPrKeys) continue;
         const int st = (it - 1) % NST;
         if (!wait_all(&v_tail, asked++ & 1) || !wait_all(&full_v[st], ((it - 1) / NST) & 1)) break;

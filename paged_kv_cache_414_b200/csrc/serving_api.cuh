@@ -1,8 +1,7 @@
 // C entry points around the 8-bit paged cache: rotary positions with the cache
 // write, decode attention, gather and block copies, and attention over packed
-// prompts.  Included by library.cu behind
-// pa_kernels.cu, whose helpers (tensor-map encoder, argument checks, wait
-// limit) it uses.
+// prompts.  Included by library.cu behind pa_kernels.cu, whose helpers
+// (tensor-map encoder, argument checks, wait limit) it uses.
 #pragma once
 
 namespace {
