@@ -326,7 +326,8 @@ int pa_paged_prefill_attention(float *out, const void *q, const void *k_cache,
  * Columns from rotary_dim on, and V, pass unchanged.
  *
  *   q_out         dtype [num_tokens, num_q_heads, head_dim] (device, written);
- *                 may be q itself with the same stride, else must not overlap it
+ *                 may be q itself with the same stride, else must not overlap
+ *                 it; never overlaps key or value
  *   q             dtype, same shape; NULL: no queries, q_out is not used
  *   key, value    dtype [num_tokens, num_kv_heads, head_dim] (device)
  *   *_stride      elements from one token's row to the next (the heads of a
@@ -349,7 +350,9 @@ int pa_paged_prefill_attention(float *out, const void *q, const void *k_cache,
  *                 positions, cos_sin and sections are not used)
  * Two tokens with the same slot in one call: which one lands is undefined.
  * num_tokens == 0 launches nothing.  num_q_heads may be any number (groups
- * play no part here).
+ * play no part here): where prompt attention needs the turned keys too, q is
+ * the query and key heads of a fused projection together, turned into q_out
+ * while the keys go into the cache.
  */
 int pa_rope_and_cache(void *q_out, const void *q, const void *key, const void *value,
                       void *k_cache, void *v_cache, const int64_t *slot_mapping,
@@ -418,8 +421,8 @@ int pa_copy_blocks_fp8(void *k_cache, void *v_cache, float *kv_scale, const int6
  *   block_tables  int32 [num_seqs, max_blocks_per_seq] (device)
  *   key_start     int32 [num_seqs + 1] (device), non-decreasing
  * Rows before key_start[0] and from key_start[num_seqs] on are left as they
- * were.  A position beyond the table sets PA_DEVERR_CONTEXT_LEN, a block id outside the pool
- * PA_DEVERR_BLOCK_ID; their rows are left as they were.
+ * were.  A position beyond the table sets PA_DEVERR_CONTEXT_LEN, a block id
+ * outside the pool PA_DEVERR_BLOCK_ID; their rows are left as they were.
  */
 int pa_gather_cache_fp8(void *key, void *value, const void *k_cache, const void *v_cache,
                         const float *kv_scale, const int32_t *block_tables,
@@ -440,7 +443,8 @@ int pa_gather_cache_fp8(void *key, void *value, const void *k_cache, const void 
  * rounded to dtype before the product with V, the output once.
  *
  *   out           dtype [num_tokens, num_q_heads, head_dim] (device, written);
- *                 rows of no sequence are left as they were
+ *                 rows of no sequence are left as they were.  Must not
+ *                 overlap the inputs
  *   q             dtype [num_tokens, num_q_heads, head_dim]
  *   key, value    dtype [num_key_tokens, num_kv_heads, head_dim]
  *   *_stride      as for pa_rope_and_cache

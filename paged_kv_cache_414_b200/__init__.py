@@ -392,7 +392,9 @@ def pa_rope_and_cache(q_out, q, key, value, k_cache, v_cache, slot_mapping, posi
     value into their slots of the 16-bit pool, in one pass.
 
     q, q_out [T, Hq, D], key, value [T, Hkv, D]: 16 bits, heads dense, tokens any multiple of 8
-    elements apart (so they may be columns of one projection); q None: keys only.
+    elements apart (so they may be columns of one projection); q None: keys only.  q may hold the
+    key heads behind the query heads, for prompt attention to read the turned keys from q_out
+    (which overlaps neither key nor value).
     positions int64 [T] or [axes, T]; cos_sin fp32 [max_position, rotary_dim], cosines then sines;
     sections: frequency pairs of each axis, e.g. (16, 24, 24) for time, height and width (default:
     one axis); interleaved: pairs are columns (2j, 2j+1) instead of (j, j + rotary_dim/2).

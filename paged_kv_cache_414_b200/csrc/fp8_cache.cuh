@@ -235,7 +235,9 @@ __global__ void __launch_bounds__(256, 3) rope_and_cache_kernel(const RopeParams
 
 // Copy-on-write copies of 8-bit blocks: a pair's K codes, V codes and scales
 // are three runs of 16-byte vectors, walked as one; each thread loads all its
-// vectors before it stores any (no destination is also a source).
+// vectors before it stores any (no destination is also a source).  Bound: HBM;
+// 2048 pairs of 16 tokens x 8 heads of 128 (138 MB in and out) take 24 us, 5.8
+// TB/s, and 37 pairs 2.9 us, a launch.
 constexpr int kCopy8Unroll = 8;
 __global__ void __launch_bounds__(256)
     copy_blocks_fp8_kernel(uint4 *k_cache, uint4 *v_cache, uint4 *kv_scale,
@@ -283,6 +285,8 @@ struct GatherParams {
 // follow from it; then K and V of every head, in an order that reads a
 // block's tokens of one head one after the other.  gridDim.y splits the
 // heads.  Rows before the first sequence and behind the last are left as they are.
+// Bound: HBM; 247 MB in and out take 48 us, 5.1 TB/s (more rows to a CTA, deeper
+// or shallower loads: the same or slower), 300 tokens 3.0 us, a launch.
 constexpr int kGatherRows = 16;
 template <typename T, int D>
 __global__ void __launch_bounds__(256) gather_cache_fp8_kernel(const GatherParams p) {

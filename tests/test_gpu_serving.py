@@ -113,3 +113,44 @@ def test_prompts_decode_fork_and_prefix(pa, cuda_device):
     close(out, attend(tq, *model[3]), 2.0 ** -4)
     assert pa.pa_device_error() == 0
     bm.close()
+
+
+def test_turned_keys_with_the_queries(pa, cuda_device):
+    """One pass turns a fused projection's query and key heads for prompt attention and fills the
+    16-bit pool; the next chunk decodes over that pool as the prompt attends over itself."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    lens = [70, 1, 33]
+    T, S = sum(lens), len(lens)
+    ang = torch.arange(128, device="cuda")[:, None] * 10000.0 ** (-torch.arange(0, D, 2, device="cuda") / D)
+    table = torch.cat([ang.cos(), ang.sin()], 1).float().contiguous()
+    qkv = torch.randn(T, HQ + 2 * HKV, D, generator=g, device="cuda").bfloat16()
+    k, v = qkv[:, HQ:HQ + HKV], qkv[:, HQ + HKV:]
+    pos = torch.cat([torch.arange(n, device="cuda") for n in lens])
+    nb = [-(-n // B) for n in lens]
+    blocks = torch.randperm(sum(nb), generator=torch.Generator().manual_seed(6)).int()
+    tables = torch.zeros(S, max(nb), dtype=torch.int32)
+    for s, own in enumerate(blocks.split(nb)):
+        tables[s, :nb[s]] = own
+    slots = torch.cat([tables[s].long()[torch.arange(n) // B] * B + torch.arange(n) % B
+                       for s, n in enumerate(lens)]).cuda()
+    kc, vc = (torch.zeros(sum(nb), HKV, B, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    turned = torch.empty(T, HQ + HKV, D, dtype=torch.bfloat16, device="cuda")
+    pa.pa_rope_and_cache(turned, qkv[:, :HQ + HKV], k, v, kc, vc, slots, pos, table)
+    # the pool's keys are those handed to prompt attention, and V's rows are v's
+    at = slots // B, slice(None), slots % B
+    assert torch.equal(kc[at], turned[:, HQ:]) and torch.equal(vc[at], v)
+    start = torch.tensor(np.cumsum([0] + lens), dtype=torch.int32, device="cuda")
+    out = torch.empty(T, HQ, D, dtype=torch.bfloat16, device="cuda")
+    scale = 1 / math.sqrt(D)
+    pa.pa_prompt_attention(out, turned[:, :HQ], turned[:, HQ:], v, start, start, scale, HKV, 70, 70)
+    # a prompt's last token attends over all of it, as decode's new token does.  Decode is fp32
+    # from the same 16-bit inputs; the prompt rounds each weight and the output to bf16, off by at
+    # most 2^-8 of themselves, together 2^-7 of the largest |v|
+    last = (start[1:] - 1).long()
+    dec = torch.empty(S, HQ, D, device="cuda")
+    ctx = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ws = pa.alloc_workspace(S, HQ, HKV, D, B, max(nb) * B)
+    pa.pa_paged_decode_attention(dec, turned[last, :HQ].contiguous(), kc, vc, tables.cuda(), ctx, scale, HKV,
+                                 workspace=ws)
+    assert (out[last].float() - dec).abs().max().item() <= 2.0 ** -7 * v.float().abs().max().item()
+    assert pa.pa_device_error() == 0
