@@ -22,8 +22,8 @@
 // tile's K is asked for as soon as the scores are made, its V after P.V, so
 // either is on its way during about half of a tile's work, and 8 to 16 warps
 // per SM cover for each other.  One elected lane issues, from warp-uniform
-// values; six lanes with a copy each took 1400 of a warp's 5900 cycles per
-// tile, and 16-byte asynchronous copies by all lanes the same.
+// values: six lanes with a copy each took 1400 cycles per tile instead of 850,
+// and so did 16-byte asynchronous copies by all lanes.
 //
 // Arithmetic.
 //   * Codes become fp16 exactly (cvt.rn.f16x2.e4m3x2) and both products are
@@ -51,7 +51,12 @@
 // or 64-byte (D = 64) rows, with which the K loads and D = 128's V loads are
 // free of bank conflicts.
 //
-// Bound: HBM, 2 D + 8 bytes per token and kv head.
+// Bound: HBM, 2 D + 8 bytes per token and kv head; held back by the
+// instructions of a tile.  Of its 4300 cycles (D = 128, eight heads, 12 warps
+// per SM) a warp waits 220 for copies, takes 740 for the scores, 2000 for
+// weights and output and 850 for the copies' bookkeeping.  375 MB of 64 / 8
+// heads take 74 us, 5.1 TB/s, and 5 us of merge; 407 MB of 256 mixed sequences
+// 79 to 84 with it.
 #pragma once
 
 #include <cuda_fp8.h>
