@@ -275,15 +275,10 @@ struct Fp8Path {
     const int g = lane >> 2, c = lane & 3;
     const float zero[4] = {0.f, 0.f, 0.f, 0.f};
     float vs[2][2];
-    const float mine = sb[(lane < B ? B : 2 * B) + lane];       // V scale of token `lane`
-    const uint32_t bits = (live >> lane) & 1 ? __float_as_uint(fabsf(mine)) : 0u;
-    const int top = scale_field(__reduce_max_sync(0xffffffffu, bits));
-    const float up = pow2_field(268 - top);
-    const float vdown = pow2_field(top - 14);   // 2^-shift of the weights
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) vs[t][x] = sb[t * (512 / B) + B + g + 8 * x] * up;
+      for (int x = 0; x < 2; ++x) vs[t][x] = sb[t * (512 / B) + B + g + 8 * x];
     if (live != 0xffffffffu) {                  // tokens that do not count
       const uint32_t mask = live >> g;
 #pragma unroll
@@ -299,11 +294,12 @@ struct Fp8Path {
           }
     }
     // ---- running maximum and sum of each head; weights (times vs) as B operands
-    float alpha[NT][HPL];
+    float alpha[NT][HPL], vdown[NT][HPL];    // vdown: 2^-shift of a head's weights
     uint32_t ph[2][NT][2], pl[2][NT][2];     // HPL = 1: hi and lo both in ph
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float hi[HPL][2][2], lo[HPL][2][2];
+      uint32_t top[HPL];                     // largest weight times vs, as bits
 #pragma unroll
       for (int e = 0; e < HPL; ++e) {
         float v = fmaxf(fmaxf(sc[0][n][0][e], sc[0][n][1][e]), fmaxf(sc[1][n][0][e], sc[1][n][1][e]));
@@ -316,17 +312,36 @@ struct Fp8Path {
         alpha[n][e] = exp2_approx(m[n][e] - ref);
         m[n][e] = mn;
         float sum = 0.f;
+        top[e] = 0;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const float pv = exp2_approx(sc[t][n][x][e] - ref);
             sum += pv;
-            const float y = pv * vs[t][x];
+            lo[e][t][x] = pv * vs[t][x];
+            top[e] = max(top[e], __float_as_uint(fabsf(lo[e][t][x])));
+          }
+        l[n][e] = l[n][e] * alpha[n][e] + sum;
+      }
+      // the exponents of both heads' largest go through the shuffles together
+      uint32_t tops = HPL == 1 ? top[0] >> 16 : __byte_perm(top[0], top[HPL - 1], 0x7632);
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1)
+        tops = __vmaxu2(tops, __shfl_xor_sync(0xffffffffu, tops, d));
+#pragma unroll
+      for (int e = 0; e < HPL; ++e) {
+        const int field = scale_field(e == 0 ? tops << 16 : tops);
+        const float up = pow2_field(268 - field);
+        vdown[n][e] = pow2_field(field - 14);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float y = lo[e][t][x] * up;
             hi[e][t][x] = __half2float(__float2half_rn(y));
             lo[e][t][x] = y - hi[e][t][x];
           }
-        l[n][e] = l[n][e] * alpha[n][e] + sum;
       }
 #pragma unroll
       for (int t = 0; t < 2; ++t)
@@ -390,7 +405,7 @@ struct Fp8Path {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
               const float add = HPL == 1 ? acc[n][2 * r] + acc[n][2 * r + 1] : acc[n][2 * r + e];
-              o[a][n][e][r] = fmaf(add, vdown, o[a][n][e][r] * alpha[n][e]);
+              o[a][n][e][r] = fmaf(add, vdown[n][e], o[a][n][e][r] * alpha[n][e]);
             }
       }
   }
