@@ -206,6 +206,15 @@ def alloc_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, m
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
 
 
+def _scratch(stream, *args):
+    """alloc_workspace on the stream that the call runs on: the memory is then neither what another
+    stream's earlier work still uses nor handed on before the call is done."""
+    if stream is None:
+        return alloc_workspace(*args)
+    with _torch().cuda.stream(stream):
+        return alloc_workspace(*args)
+
+
 def pa_paged_decode_attention(out, q, k_cache, v_cache, block_tables, context_lens, scale,
                               num_kv_heads, max_context_len=None, workspace=None, stream=None):
     """out[s, h] = softmax(scale * q[s, h] K_s^T) V_s over the sequence's cached tokens."""
@@ -222,7 +231,7 @@ def pa_paged_decode_attention(out, q, k_cache, v_cache, block_tables, context_le
     if max_context_len is None:
         max_context_len = maxb * B
     if workspace is None:
-        workspace = alloc_workspace(S, Hq, Hkv, D, B, max_context_len, q.device)
+        workspace = _scratch(stream, S, Hq, Hkv, D, B, max_context_len, q.device)
     st = lib().pa_paged_decode_attention(
         _dev(out, "out", torch.float32), _dev(q, "q", k_cache.dtype), _dev(k_cache, "k_cache"),
         _dev(v_cache, "v_cache", k_cache.dtype), _dev(block_tables, "block_tables", torch.int32),
@@ -280,7 +289,7 @@ def pa_decode_step(out, q, k_new, v_new, k_cache, v_cache, block_tables, context
     if max_context_len is None:
         max_context_len = maxb * B
     if workspace is None:
-        workspace = alloc_workspace(S, Hq, Hkv, D, B, max_context_len, q.device)
+        workspace = _scratch(stream, S, Hq, Hkv, D, B, max_context_len, q.device)
     dt = k_cache.dtype
     st = lib().pa_decode_step(
         _dev(out, "out", torch.float32), _dev(q, "q", dt), _dev(k_new, "k_new", dt),

@@ -13,6 +13,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -156,7 +157,9 @@ class Call {
   }
 
   // The caller's workspace, or scratch of `bytes` that lives until the call is
-  // launched (the allocator keeps it for the stream that uses it).
+  // launched.  It is allocated on the stream that the call runs on: the memory is
+  // then neither what another stream's earlier work still uses nor handed on
+  // before the call is done.
   void *workspace(int i, int stream_arg, size_t bytes, size_t *have) {
     if (!none(i)) {
       const at::Tensor &t = tensor(i, "workspace");
@@ -168,10 +171,11 @@ class Call {
     }
     *have = bytes;
     if (bytes == 0) return nullptr;
+    const c10::cuda::CUDAStreamGuard on(
+        none(stream_arg) ? c10::cuda::getCurrentCUDAStream(device_)
+                         : c10::cuda::getStreamFromExternal(stream(stream_arg), device_));
     scratch_ = at::empty({(int64_t)bytes},
                          at::TensorOptions().dtype(at::kByte).device(at::kCUDA, device_));
-    if (!none(stream_arg))   // allocated on the current stream, used on another
-      scratch_.record_stream(c10::cuda::getStreamFromExternal(stream(stream_arg), device_));
     return scratch_.data_ptr();
   }
 
