@@ -738,6 +738,11 @@ __global__ void __launch_bounds__(NW * 32, fp8_ctas(NT, HPL))
                             c_lo, merge ? c_hi - c_lo + 1 : 0);
   }
 
+  // every lane waits; the warp goes on only if all of them saw the phase (lanes
+  // whose limits ran out alone would leave the others' shuffles without a source)
+  auto wait_all = [&](uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, p.wait_ns));
+  };
   Fp8Path<D, NT, HPL> st;
   st.init(lane);
   bool seg_from0 = false;
@@ -745,7 +750,7 @@ __global__ void __launch_bounds__(NW * 32, fp8_ctas(NT, HPL))
   for (int i = 0; i < ntiles; ++i) {
     const Fp8Tile tn = i + 1 < ntiles ? next_tile(i + 1) : ti;
     const float *sc = scales + (i & 1) * kF8ScaleFloats;
-    if (!mbar_wait_bounded(kbar, i & 1, p.wait_ns)) {
+    if (!wait_all(kbar, i & 1)) {
       if (lane == 0) flag_error(PA_DEVERR_TIMEOUT);
       // copies still in flight land before the warp leaves
       mbar_wait_bounded(kbar, i & 1, kDrainLimitNs);
@@ -759,7 +764,7 @@ __global__ void __launch_bounds__(NW * 32, fp8_ctas(NT, HPL))
     }
     if (ti.live) st.scores(kbuf, sc, B, lane);
     if (i + 1 < ntiles) copy_k(i + 1, tn);
-    if (!mbar_wait_bounded(vbar, i & 1, p.wait_ns)) {
+    if (!wait_all(vbar, i & 1)) {
       if (lane == 0) flag_error(PA_DEVERR_TIMEOUT);
       mbar_wait_bounded(vbar, i & 1, kDrainLimitNs);
       if (i + 1 < ntiles) mbar_wait_bounded(kbar, (i + 1) & 1, kDrainLimitNs);
