@@ -15,6 +15,7 @@
 #include "cache_ops.cuh"
 #include "decode_attention.cuh"
 #include "prefill_attention.cuh"
+#include "smem_limit.h"
 
 namespace {
 
@@ -64,6 +65,12 @@ std::atomic<unsigned long long> g_wait_limit_ns{kDefaultWaitLimitNs};
 std::atomic<int> g_tune_nstage{0};
 std::atomic<int> g_tune_ctas{0};
 std::atomic<int> g_tune_min_tiles{0};
+
+template <typename Kernel>
+bool set_smem(Kernel kern, size_t bytes) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
+         cudaSuccess;
+}
 
 struct DecodeLayout {
   int nstage, ctas_per_sm, grid, w_total, min_tiles;
@@ -178,13 +185,8 @@ int launch_decode(const DecodeArgs &a, int dev, int sms) {
   choose_layout(D, B, G, sms, regs, &L);
   if (a.workspace_bytes < L.workspace) return PA_ERR_WORKSPACE;
 
-  static std::atomic<size_t> attr_set[kMaxDevices];
-  if (attr_set[dev].load() < L.smem) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L.smem) !=
-        cudaSuccess)
-      return PA_ERR_CUDA;
-    attr_set[dev].store(L.smem);
-  }
+  static pa::SmemLimit<kMaxDevices> limit;
+  if (!limit.raise(dev, L.smem, [&](size_t n) { return set_smem(kern, n); })) return PA_ERR_CUDA;
   CUtensorMap kmap, vmap;
   const long long rows = (long long)a.num_blocks * a.num_kv_heads * B;
   if (!encode_pool_map(&kmap, a.k_cache, rows, D, B) ||

@@ -161,13 +161,8 @@ int launch_decode_fp8(pa::DecodeFp8Params &p, const CUtensorMap &kmap, const CUt
   const size_t smem = 1024 + (size_t)kWarpsPerCta * pa::fp8_warp_bytes(D, G);   // 1024: alignment
   const int most = pa::fp8_ctas(NT, HPL), want = g_tune_ctas.load();
   const int ctas = want > 0 ? std::min(want, most) : most;
-  static std::atomic<size_t> attr_set[kMaxDevices];
-  if (attr_set[dev].load() < smem) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-        cudaSuccess)
-      return PA_ERR_CUDA;
-    attr_set[dev].store(smem);
-  }
+  static pa::SmemLimit<kMaxDevices> limit;
+  if (!limit.raise(dev, smem, [&](size_t n) { return set_smem(kern, n); })) return PA_ERR_CUDA;
   const long long pairs = (long long)p.num_seqs * p.num_kv_heads;
   const long long tiles = (max_context + pa::kF8Tile - 1) / pa::kF8Tile + 1;   // of a pair, at most
   // Short contexts are not cut (a warp takes a pair's tiles in less time than a
