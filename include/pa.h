@@ -454,6 +454,8 @@ int pa_gather_cache_fp8(void *key, void *value, const void *k_cache, const void 
  *                 A sequence that leaves the tensors, or has more queries than
  *                 max_query_len or more keys than max_key_len, is not computed
  *                 and sets PA_DEVERR_CONTEXT_LEN
+ *                 (with max_query_len 0, query_start may be NULL: nothing is
+ *                 looked at or written)
  *   workspace     pa_prompt_attention_workspace_bytes(...) bytes, 256-byte
  *                 aligned; that is 0 (workspace may be NULL) unless the queries
  *                 are too few to occupy the GPU and the keys are split

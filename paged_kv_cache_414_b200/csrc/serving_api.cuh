@@ -247,6 +247,11 @@ PromptPlan plan_prompt(int num_seqs, int num_tokens, int num_q_heads, int num_kv
                        int head_dim, int max_query, int max_key, int sms) {
   PromptPlan pl;
   pl.tq = pa::kPrRows / (num_q_heads / num_kv_heads);
+  if (max_query == 0) {   // one CTA, which reports sequences that have queries all the same
+    pl.units = pl.pieces = pl.piece_tiles = 1;
+    pl.workspace = 0;
+    return pl;
+  }
   const long long w = 2 * pl.tq;
   const long long pairs = std::min((long long)num_seqs * ((max_query + w - 1) / w),
                                    num_tokens / w + num_seqs);
@@ -500,7 +505,7 @@ int pa_prompt_attention(void *out, const void *q, const void *key, const void *v
   const int bad = check_prompt(num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim,
                                max_query_len, max_key_len);
   if (bad != PA_OK) return bad;
-  if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return PA_OK;
+  if (num_seqs == 0 || num_tokens == 0 || (max_query_len == 0 && !query_start)) return PA_OK;
   if (!out || !q || !query_start || !key_start || (num_key_tokens > 0 && (!key || !value)))
     return PA_ERR_ARG;
   if (!aligned(out, 16) || !aligned(q, 16) || !aligned(key, 16) || !aligned(value, 16) ||
