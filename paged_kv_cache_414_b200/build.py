@@ -6,6 +6,7 @@ extension module that marshals torch tensors for the shortest calls.
 """
 from __future__ import annotations
 
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -51,11 +52,27 @@ def up_to_date() -> bool:
     return _newer(LIB, _inputs())
 
 
-def build_calls(force: bool = False) -> str:
-    """The extension module, against the headers of the installed torch."""
+def _torch_version():
+    """The installed torch's version, without importing it; None if there is none."""
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        return None
+
+
+def build_calls(force: bool = False) -> str | None:
+    """The extension module, against the headers of the installed torch; None without torch, which
+    the library itself does not need."""
     src = os.path.join(CSRC, "binding.cpp")
-    if not force and _newer(CALLS, [src, os.path.join(INCLUDE, "pa.h")]):
-        return CALLS
+    version = _torch_version()
+    if version is None:
+        return None
+    stamp = os.path.join(BUILD_DIR, "_calls.torch")     # the version it was built against
+    if os.path.exists(stamp):
+        with open(stamp) as f:
+            same = f.read() == version
+        if same and not force and _newer(CALLS, [src, os.path.join(INCLUDE, "pa.h")]):
+            return CALLS
     import torch
     home = os.path.dirname(torch.__file__)
     inc = os.path.join(home, "include")
@@ -72,11 +89,20 @@ def build_calls(force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("g++ failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
     os.replace(tmp, CALLS)
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    with open(stamp, "w") as f:
+        f.write(version)
     return CALLS
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    """The library, then the extension module; the library's path."""
+    lib = build_library(force, verbose)
     build_calls(force)
+    return lib
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)
