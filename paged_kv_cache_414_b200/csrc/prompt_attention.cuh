@@ -9,11 +9,11 @@
 // Work unit: (sequence, pair of query tiles, kv head, piece of the keys).  A
 // query tile is 128 rows = tq = 128 / G tokens x the G heads of one kv head;
 // tiles A and B (2 tq consecutive tokens) share every K/V tile of 128 keys.
-// Units are numbered longest first over all sequences -- found in the kernel
-// by a search over the lengths -- and CTAs, one per SM, take them in that
-// order: the first by blockIdx, the next by cancelling CTAs that have not been
-// launched yet (clusterlaunchcontrol), so that loads, the tensor-memory
-// allocation and the barriers of one unit run on into the next.
+// Units are numbered longest first over all sequences -- found in the kernel by
+// a search over the lengths that goes on from a CTA's last unit -- and CTAs, one
+// per SM, take them in that order: the first by blockIdx, the next by cancelling
+// CTAs that have not been launched yet (clusterlaunchcontrol), so that loads, the
+// tensor-memory allocation and the barriers of one unit run on into the next.
 //
 //   warps 0-3   softmax and output of tile A, one thread per row
 //   warps 4-7   the same for tile B
@@ -34,13 +34,16 @@
 // tensor cores' rate (the exponentials' unit is busy for as long).  One prompt
 // of 8192 tokens, 32 / 8 heads of 128: 459 us, 1.2 PFLOP/s of visible pairs;
 // 16 prompts of 64 to 2048 tokens, 40 heads: 209 us, 0.69 (their units have few
-// tiles, and the diagonal ones count half).  Measured and left: a polynomial on the FMA units for a
-// quarter of the exponentials (498 us), scores in halves of 64 keys with two in
-// flight (590), two threads to a row (783), the next unit's first scores before
-// this one's last P.V (465), heads in groups whose K/V fit the L2 cache (as
-// before or slower), masks as selects in registers instead of a pass over the
-// tile (457, with spills).
+// tiles, and the diagonal ones count half); 256 prompts of 70 tokens, 32 / 8
+// heads of 128: 124 us, 4000 of them 1.91 ms (the units' fixed costs).  Measured
+// and left: a polynomial on the FMA units for a quarter of the exponentials (498
+// us), scores in halves of 64 keys with two in flight (590), two threads to a row
+// (783), the next unit's first scores before this one's last P.V (465), heads in
+// groups whose K/V fit the L2 cache (as before or slower), masks as selects in
+// registers instead of a pass over the tile (457, with spills).
 #pragma once
+
+#include <limits.h>
 
 #include "prefill_attention.cuh"
 #include "prompt_umma.cuh"
@@ -146,13 +149,24 @@ __device__ __forceinline__ int2 prompt_order(const PromptParams &p, const Prompt
   return make_int2(max(0, q.L - q.C) / w, (q.C + w - 1) / w);
 }
 
+// Where the last search ended: the units of order `level` begin with number
+// `above`, and `seen` of them are of sequences before i0.  A CTA's unit numbers
+// grow, so the next search goes on from there: with every search from the
+// start, the cost of a call grew with the square of the number of sequences
+// (4000 prompts of 70 tokens took 43 ms).
+struct PromptCursor {
+  int level = -1, above = 0, i0 = 0, seen = 0;
+  int total = INT_MAX;   // units in all, once a search has gone past the last one
+};
+
 // Unit number v in order of decreasing length (ties by sequence): its pair and
 // sequence, or false past the last one.  A whole warp; lane i holds sequence i
 // and its order, the further ones' orders are in `cache` as far as that goes.
 __device__ __forceinline__ bool prompt_find(const PromptParams &p, const int2 *cache,
                                             const PromptSeq &mine, int2 order, int v,
-                                            PromptSeq *found, int *pair) {
+                                            PromptCursor &at, PromptSeq *found, int *pair) {
   const int lane = threadIdx.x & 31;
+  if (v >= at.total) return false;
   auto further = [&](int i) {
     return i < kPrSeqCache ? cache[i] : prompt_order(p, prompt_seq(p, i, false));
   };
@@ -166,45 +180,61 @@ __device__ __forceinline__ bool prompt_find(const PromptParams &p, const int2 *c
     return __reduce_add_sync(0xffffffffu, n);
   };
   // at_least(lo) > v >= at_least(hi) = above, once lo is known not to be -1
-  int lo = -1, hi = (p.max_query + p.max_key) / (2 * p.tq) + 2, above = 0;
+  int hi = (p.max_query + p.max_key) / (2 * p.tq) + 2, above = 0;
   if (p.num_seqs <= 32) hi = __reduce_max_sync(0xffffffffu, order.x + order.y);
+  bool known = at.level >= 0 && v >= at.above + at.seen, next = false;
 #pragma unroll 1
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1, n = at_least(mid);
-    if (n > v) {
-      lo = mid;
-    } else {
-      hi = mid;
-      above = n;
-    }
-  }
-  if (lo < 0) return false;
-  int left = v - above;
+  while (true) {
+    if (!known) {
+      int lo = -1;
 #pragma unroll 1
-  for (int i0 = 0; i0 < p.num_seqs; i0 += 32) {
-    const int i = i0 + lane;
-    const int2 q = i0 == 0 ? order : (i < p.num_seqs ? further(i) : make_int2(0, 0));
-    const bool has = q.x <= lo && lo < q.x + q.y;
-    const unsigned who = __ballot_sync(0xffffffffu, has);
-    const int many = __popc(who);
-    if (left < many) {
-      const unsigned which = __ballot_sync(
-          0xffffffffu, has && __popc(who & ((1u << lane) - 1u)) == left);
-      const int src = __ffs(which) - 1;
-      *pair = lo - __shfl_sync(0xffffffffu, q.x, src);
-      if (i0 == 0) {
-        found->q0 = __shfl_sync(0xffffffffu, mine.q0, src);
-        found->C = __shfl_sync(0xffffffffu, mine.C, src);
-        found->k0 = __shfl_sync(0xffffffffu, mine.k0, src);
-        found->L = __shfl_sync(0xffffffffu, mine.L, src);
-      } else {
-        *found = prompt_seq(p, i0 + src, false);
+      while (hi - lo > 1) {
+        const int mid = next ? hi - 1 : (lo + hi) >> 1, n = at_least(mid);
+        next = false;
+        if (n > v) {
+          lo = mid;
+        } else {
+          hi = mid;
+          above = n;
+        }
       }
-      return true;
+      if (lo < 0) {
+        at.total = above;
+        return false;
+      }
+      at.level = lo, at.above = above, at.i0 = 0, at.seen = 0;
     }
-    left -= many;
+    const int lo = at.level;
+    int left = v - at.above - at.seen;
+#pragma unroll 1
+    for (; at.i0 < p.num_seqs; at.i0 += 32) {
+      const int i0 = at.i0, i = i0 + lane;
+      const int2 q = i0 == 0 ? order : (i < p.num_seqs ? further(i) : make_int2(0, 0));
+      const bool has = q.x <= lo && lo < q.x + q.y;
+      const unsigned who = __ballot_sync(0xffffffffu, has);
+      const int many = __popc(who);
+      if (left < many) {
+        const unsigned which = __ballot_sync(
+            0xffffffffu, has && __popc(who & ((1u << lane) - 1u)) == left);
+        const int src = __ffs(which) - 1;
+        *pair = lo - __shfl_sync(0xffffffffu, q.x, src);
+        if (i0 == 0) {
+          found->q0 = __shfl_sync(0xffffffffu, mine.q0, src);
+          found->C = __shfl_sync(0xffffffffu, mine.C, src);
+          found->k0 = __shfl_sync(0xffffffffu, mine.k0, src);
+          found->L = __shfl_sync(0xffffffffu, mine.L, src);
+        } else {
+          *found = prompt_seq(p, i0 + src, false);
+        }
+        return true;
+      }
+      left -= many;
+      at.seen += many;
+    }
+    // the order is through: v is in one below, mostly the next
+    hi = lo, above = at.above + at.seen;
+    known = false, next = true;
   }
-  return false;
 }
 
 // Tiles of 128 keys that the tokens up to position `last` see.
@@ -371,6 +401,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       }
       __syncwarp();
       int block = blockIdx.x, made = 0, asked = 0;
+      PromptCursor cursor;
       while (true) {
         PromptUnit u;
         u.n[0] = -1;
@@ -380,7 +411,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           const int kh = rest % p.num_kv_heads, v = rest / p.num_kv_heads;
           PromptSeq q;
           int pair;
-          if (prompt_find(p, seqs, mine, order, v, &q, &pair)) {
+          if (prompt_find(p, seqs, mine, order, v, cursor, &q, &pair)) {
             const PromptPair w = prompt_pair(p, q, pair);
             const int j0 = piece * p.piece_tiles;
             u.n[0] = min(max(w.tiles[0] - j0, 0), p.piece_tiles);
