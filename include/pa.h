@@ -392,9 +392,9 @@ int pa_rope_and_cache_fp8(void *q_out, const void *q, const void *key, const voi
  * workspace (pa_paged_decode_workspace_bytes) and errors, plus kv_scale; q of
  * dtype, out fp32.  Accumulated in fp32; a weight times the scale of its V row
  * is carried to 2^-22 of itself or 2^-39 of the largest such product among its
- * tile of 32 tokens, so the output is that of the cached values (code * scale)
- * to ~1e-6 of sum_t w_t |v_t|, however far the rows of V differ in size.  Of
- * pa_decode_tuning the CTAs per SM and the tiles per warp apply; contexts that
+ * tile of 32 tokens, whichever is more, so the output is that of the cached
+ * values (code * scale) to ~1e-6 of the terms it is the sum of, however far the
+ * rows of V differ in size.  Of pa_decode_tuning the CTAs per SM and the tiles per warp apply; contexts that
  * max_context_len says are short are not split at all.
  */
 int pa_paged_decode_attention_fp8(float *out, const void *q, const void *k_cache,

@@ -52,16 +52,18 @@
 // free of bank conflicts.
 //
 // Bound: HBM, 2 D + 8 bytes per token and kv head; held back by the
-// instructions of a tile.  Of its 4300 cycles (D = 128, eight heads, 12 warps
-// per SM) a warp waits 220 for copies, takes 740 for the scores, 2000 for
-// weights and output and 850 for the copies' bookkeeping.  375 MB of 64 / 8
-// heads take 74 us, 5.1 TB/s, and 5 us of merge; 407 MB of 256 mixed sequences
-// 79 to 84 with it.
+// instructions of a tile.  Of its 4100 cycles (D = 128, eight heads, 12 warps
+// per SM) a warp waits 380 for copies, takes 900 for the scores, 2030 for
+// weights and output and 820 for the copies' bookkeeping.  375 MB of 64 / 8
+// heads take 71 us, 5.3 TB/s, and 79 with the merge in a loop of calls; 407 MB
+// of 256 mixed sequences 79 to 80 with it.  Groups above eight pay for their
+// registers (two CTAs per SM): 375 MB of 128 / 8 heads take 116 us.
 #pragma once
 
 #include <cuda_fp8.h>
 
 #include "decode_attention.cuh"
+#include "prefill_attention.cuh"   // fast_exp2
 
 namespace pa {
 
@@ -111,13 +113,6 @@ __device__ __forceinline__ uint32_t e4m3x2_hi_to_f16x2(uint32_t x) {
       "cvt.rn.f16x2.e4m3x2 %0, hi;\n\t}"
       : "=r"(y)
       : "r"(x));
-  return y;
-}
-
-// 2^x by the hardware approximation (2 ulp, results below 2^-126 are zero).
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -309,7 +304,7 @@ struct Fp8Path {
         const float mn = fmaxf(m[n][e], v);
         // all scores so far -inf (a -inf in q or K): weights of 0, not NaN
         const float ref = mn == -INFINITY ? 0.f : mn;
-        alpha[n][e] = exp2_approx(m[n][e] - ref);
+        alpha[n][e] = fast_exp2(m[n][e] - ref);
         m[n][e] = mn;
         float sum = 0.f;
         top[e] = 0;
@@ -317,7 +312,7 @@ struct Fp8Path {
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const float pv = exp2_approx(sc[t][n][x][e] - ref);
+            const float pv = fast_exp2(sc[t][n][x][e] - ref);
             sum += pv;
             lo[e][t][x] = pv * vs[t][x];
             top[e] = max(top[e], __float_as_uint(fabsf(lo[e][t][x])));

@@ -26,7 +26,7 @@
 //               another sequence's NaN, and 0 x NaN would reach every row)
 //
 // P replaces S in tensor memory, in the inputs' 16-bit type: rounding the
-// weights (2^-9 or 2^-12 each, independent) costs about as much as rounding
+// weights (at most 2^-8 or 2^-11 each, independent) costs about as much as rounding
 // the output does.  Maximum, sum and O are fp32.  O is rescaled only when a
 // row's maximum grows by more than 2^8 (weights then stay below 2^8).
 //
