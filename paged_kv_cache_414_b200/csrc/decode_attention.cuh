@@ -903,7 +903,8 @@ __global__ void __launch_bounds__(NW * 32, NT == 0 ? 3 : 2)
   for (long long i = 0; i < ntiles; ++i) {
     const int stage = (int)(i % nstage);
     const uint32_t parity = (uint32_t)((i / nstage) & 1);
-    if (!mbar_wait_bounded(&bars[stage], parity, p.wait_ns)) {
+    // all lanes or none go on: the next shuffles take part of every lane
+    if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bars[stage], parity, p.wait_ns))) {
       if (lane == 0) flag_error(PA_DEVERR_TIMEOUT);
       // drain the copies still in flight -- this tile's and those issued
       // after it -- so that none lands after the warp has left
