@@ -211,7 +211,10 @@ def _scratch(stream, *args):
     stream's earlier work still uses nor handed on before the call is done."""
     if stream is None:
         return alloc_workspace(*args)
-    with _torch().cuda.stream(stream):
+    cuda = _torch().cuda
+    if not isinstance(stream, cuda.Stream):      # another library's, known by its handle
+        stream = cuda.ExternalStream(stream.cuda_stream)
+    with cuda.stream(stream):
         return alloc_workspace(*args)
 
 

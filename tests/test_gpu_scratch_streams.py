@@ -1,6 +1,8 @@
 """Calls given a stream and no workspace: the scratch that the binding makes for them is that
 stream's.  Memory that the current stream has freed but still uses is not written, and what the
 current stream allocates after the call is not the scratch of a call that has yet to run."""
+import types
+
 import pytest
 import torch
 
@@ -72,3 +74,20 @@ def test_scratch_is_the_calls_stream_s(pa, cuda_device, name):
     torch.cuda.synchronize()
     assert (z == 7).all() and torch.equal(later, want)
     assert pa.pa_device_error() == 0
+
+
+@pytest.mark.parametrize("name", ["decode_fp8", "prompt", "decode", "decode_step"])
+def test_a_stream_known_by_its_handle(pa, cuda_device, name):
+    """Any object with a cuda_stream names the stream, the default stream among them."""
+    call, made, _ = make(name, pa)
+    want = made()
+    call(want, None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, torch.cuda.default_stream(), torch.cuda.ExternalStream(side.cuda_stream)):
+        for given in (stream, types.SimpleNamespace(cuda_stream=stream.cuda_stream)):
+            got = made()
+            torch.cuda.synchronize()
+            call(got, given)
+            torch.cuda.synchronize()
+            assert torch.equal(got, want)
